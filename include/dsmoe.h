@@ -549,6 +549,80 @@ dsmoe_status dsmoe_route_noalloc(const dsmoe_cfg* cfg, int32_t T, const void* x,
                                  const float* b, int32_t* topk_idx, float* gates, int32_t* counts, float* f,
                                  float* P, void* stream);
 
+/*
+ * The 8-bit path. A matrix in 8 bits is a tensor of e4m3 values and one power of two per
+ * block of 128 values along the reduction dimension (token rows: 1 x 128 blocks, expert
+ * weights: 128 x 128), stored as an e8m0 byte s that stands for 2^(s-127): the smallest
+ * 2^k with max|block| <= 448 2^k and k >= -126. A row of C values has
+ * S(C) = 4 ceil(C / 512) scale bytes (dsmoe_q8_scale_cols); those past ceil(C / 128) hold
+ * 127 (1.0). An entry is its value times its block's scale; values are rounded to nearest
+ * even. A block with an infinity or a NaN becomes NaN as a whole (byte 255, values 0x7F).
+ *
+ *   rows     values [R, C], scales [R, S(C)]
+ *   weights  values [E, N, K], scales [E, ceil(N / 128), S(K)]
+ *
+ * Sizes: C and K multiples of 16, at most 32768; E at most 512; R at most 2^30. All device
+ * pointers are 16-byte aligned and outputs must not overlap inputs unless said. The handle
+ * gives the device, the status word and the wait limit; except where d or T is named, its
+ * configuration does not matter.
+ *
+ * dsmoe_q8_quantize -- x bf16 [R, C] to 8-bit rows. R == 0 does nothing.
+ * dsmoe_q8_quantize_weights -- W bf16 [E, N, K] to 8-bit weights.
+ */
+int32_t dsmoe_q8_scale_cols(int32_t C);
+dsmoe_status dsmoe_q8_quantize(dsmoe_handle* h, int64_t R, int32_t C, const void* x, void* q, void* scales,
+                               void* stream);
+dsmoe_status dsmoe_q8_quantize_weights(dsmoe_handle* h, int32_t E, int32_t N, int32_t K, const void* W, void* q,
+                                       void* scales, void* stream);
+
+/*
+ * The root-mean-square norm in front of the layer, for T <= max_tokens rows of d = d_model:
+ *   r = bf16(x + residual), u = bf16(r w / sqrt(mean(r^2) + eps)), and the 8-bit rows of u
+ * (statistics in fp32; the 8-bit rows are exactly dsmoe_q8_quantize of u).
+ *
+ * dsmoe_norm_q8
+ *     x         bf16 [T, d]
+ *     residual  bf16 [T, d] or NULL (then r = x)
+ *     w         bf16 [d], eps >= 0
+ *     r         bf16 [T, d] out, or NULL; may be x or residual itself
+ *     u         bf16 [T, d] out, or NULL (at least one of u and q)
+ *     q, scales 8-bit rows out [T, d], [T, S(d)], or both NULL
+ * dsmoe_norm_backward -- for dy = dL/du (e.g. the dx of dsmoe_backward_experts; a gradient
+ *   of the 8-bit rows passes straight through their rounding) and dres = dL/dr of every
+ *   other use of r (or NULL):
+ *     dy   fp32 [T, d], dres bf16 [T, d] or NULL, r bf16 [T, d] and w, eps of the forward
+ *     dx   bf16 [T, d] out = dres + rstd w dy - r rstd^3 mean(w dy r): the gradient of x and of
+ *          the residual alike, rounded once (an earlier layer takes it as its dh); may be dres
+ *     dw   fp32 [d] out = sum_t dy r rstd, in a fixed order (deterministic)
+ *   Uses the handle's workspace, as its forwards do. T == 0 writes dw = 0.
+ */
+dsmoe_status dsmoe_norm_q8(dsmoe_handle* h, int32_t T, const void* x, const void* residual, const void* w, float eps,
+                           void* r, void* u, void* q, void* scales, void* stream);
+dsmoe_status dsmoe_norm_backward(dsmoe_handle* h, int32_t T, const float* dy, const void* dres, const void* r,
+                                 const void* w, float eps, void* dx, float* dw, void* stream);
+
+/*
+ * Grouped products of 8-bit rows with 8-bit expert weights: rows offsets[e] .. offsets[e+1]
+ * of a [R, K] use expert e's weights (offsets int32 [E + 1] on the device, not decreasing,
+ * within [0, R]; E = 1 with {0, R} is a plain product). Output rows outside
+ * [offsets[0], offsets[E]) are left as they were. Products of e4m3 values and scales are
+ * summed in fp32. Offsets outside [0, R] are clipped to it and a group that would end
+ * before it starts is empty, so that nothing outside the tensors is touched; what
+ * decreasing offsets leave in rows that two groups share is undefined.
+ *
+ * dsmoe_q8_matmul -- out bf16 [R, N] = a W^T, rounded once; N a multiple of 8.
+ * dsmoe_q8_gated_matmul -- q, scales: the 8-bit rows [R, N] of SiLU(a W_gate^T) (a W_up^T),
+ *   taken from the fp32 values (what dsmoe_q8_matmul then reads as its rows); N a multiple
+ *   of 16.
+ */
+dsmoe_status dsmoe_q8_matmul(dsmoe_handle* h, int32_t E, int64_t R, int32_t N, int32_t K, const int32_t* offsets,
+                             const void* a, const void* a_scales, const void* W, const void* W_scales, void* out,
+                             void* stream);
+dsmoe_status dsmoe_q8_gated_matmul(dsmoe_handle* h, int32_t E, int64_t R, int32_t N, int32_t K,
+                                   const int32_t* offsets, const void* a, const void* a_scales, const void* W_gate,
+                                   const void* gate_scales, const void* W_up, const void* up_scales, void* q,
+                                   void* scales, void* stream);
+
 #ifdef __cplusplus
 }  /* extern "C" */
 #endif

@@ -35,6 +35,8 @@ ABI_FUNCTIONS = (
     "dsmoe_round_bf16", "dsmoe_backward_gates", "dsmoe_backward_router", "dsmoe_ep_route", "dsmoe_ep_experts",
     "dsmoe_ep_combine", "dsmoe_forward_host_async", "dsmoe_host_join", "dsmoe_host_sync", "dsmoe_set_training",
     "dsmoe_backward_experts", "dsmoe_backward_weights", "dsmoe_gemm_role_cycles",
+    "dsmoe_q8_scale_cols", "dsmoe_q8_quantize", "dsmoe_q8_quantize_weights", "dsmoe_norm_q8", "dsmoe_norm_backward",
+    "dsmoe_q8_matmul", "dsmoe_q8_gated_matmul",
 )
 ROLE_CTAS, ROLE_SLOTS = 160, 9
 ROLE_KINDS = ("gemm_down", "gemm_gate_up", "shared_down", "shared_gate_up", "weight_grad")
@@ -108,6 +110,13 @@ def _load():
         "dsmoe_ep_combine": (ctypes.c_int, [vp, i32] + [vp] * 7 + [vp]),
         "dsmoe_backward_router": (ctypes.c_int, [vp, i32, vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp,
                                                  vp]),
+        "dsmoe_q8_scale_cols": (i32, [i32]),
+        "dsmoe_q8_quantize": (ctypes.c_int, [vp, i64, i32] + [vp] * 3 + [vp]),
+        "dsmoe_q8_quantize_weights": (ctypes.c_int, [vp, i32, i32, i32] + [vp] * 3 + [vp]),
+        "dsmoe_norm_q8": (ctypes.c_int, [vp, i32, vp, vp, vp, ctypes.c_float] + [vp] * 4 + [vp]),
+        "dsmoe_norm_backward": (ctypes.c_int, [vp, i32, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp]),
+        "dsmoe_q8_matmul": (ctypes.c_int, [vp, i32, i64, i32, i32] + [vp] * 6 + [vp]),
+        "dsmoe_q8_gated_matmul": (ctypes.c_int, [vp, i32, i64, i32, i32] + [vp] * 9 + [vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -180,13 +189,18 @@ def dsmoe_workspace_bytes(cfg: DsmoeCfg) -> int:
     return n.value
 
 
+_handles: Dict[int, tuple] = {}  # live handles: (device, d_model)
+
+
 def dsmoe_create(cfg: DsmoeCfg, device: int = 0) -> int:
     h = ctypes.c_void_p()
     _check(_lib.dsmoe_create(ctypes.byref(cfg), int(device), ctypes.byref(h)), "dsmoe_create")
+    _handles[h.value] = (int(device), cfg.d_model)
     return h.value
 
 
 def dsmoe_destroy(handle: int) -> None:
+    _handles.pop(handle, None)
     _lib.dsmoe_destroy(handle)
 
 
@@ -383,6 +397,102 @@ def dsmoe_sequence_balance(handle, T, seq_len, topk_idx, scores, beta, f_seq, p_
 def dsmoe_bias_update(handle, T, counts, alpha, b, stream=None):
     _check(_lib.dsmoe_bias_update(handle, int(T), _ptr(counts), float(alpha), _ptr(b), _stream(stream)),
            "dsmoe_bias_update")
+
+
+# ---- the 8-bit path. Byte tensors (e4m3 values, e8m0 scales) may be of any one-byte dtype, e.g.
+# torch.float8_e4m3fn and torch.float8_e8m0fnu.
+_BYTES = ("torch.float8_e4m3fn", "torch.float8_e8m0fnu", "torch.uint8", "torch.int8")
+_DTYPES = {"bf16": ("torch.bfloat16",), "f32": ("torch.float32",), "i32": ("torch.int32",), "q8": _BYTES}
+
+
+def _take(where: str, handle, stream, **tensors):
+    """Check the torch tensors of a call (name -> (tensor, kind, elements); raw addresses pass) and
+    return their addresses in order, and the stream: the caller's, or the current stream of
+    the handle's device."""
+    device = _handles[handle][0] if handle in _handles else None
+    ptrs = []
+    for name, (t, kind, n) in tensors.items():
+        if t is None or isinstance(t, int):
+            ptrs.append(t)
+            continue
+        if str(t.dtype) not in _DTYPES[kind]:
+            raise DsmoeError(DSMOE_ERR_INVALID_ARG, where, f"{name} is {t.dtype}, not {' or '.join(_DTYPES[kind])}")
+        if t.numel() != n:
+            raise DsmoeError(DSMOE_ERR_INVALID_ARG, where, f"{name} has {t.numel()} elements, not {n}")
+        if not t.is_contiguous():
+            raise DsmoeError(DSMOE_ERR_INVALID_ARG, where, f"{name} is not contiguous")
+        if not t.is_cuda or (device is not None and t.device.index != device):
+            raise DsmoeError(DSMOE_ERR_INVALID_ARG, where, f"{name} is on {t.device}, not on the handle's GPU")
+        ptrs.append(t.data_ptr())
+    if stream is None and device is not None:
+        import torch
+        stream = torch.cuda.current_stream(device).cuda_stream
+    return ptrs, _stream(stream)
+
+
+def _norm_width(where, handle, w) -> int:
+    """d of the handle's rows, which w has to match."""
+    d = w.numel() if hasattr(w, "numel") else 0
+    if handle in _handles and hasattr(w, "numel") and d != _handles[handle][1]:
+        raise DsmoeError(DSMOE_ERR_INVALID_ARG, where, f"w has {d} elements, not d_model = {_handles[handle][1]}")
+    return _handles[handle][1] if handle in _handles else d
+
+
+def dsmoe_q8_scale_cols(C: int) -> int:
+    """Scale bytes of a row of C values: 4 ceil(C / 512)."""
+    return int(_lib.dsmoe_q8_scale_cols(int(C)))
+
+
+def dsmoe_q8_quantize(handle, R, C, x, q, scales, stream=None) -> None:
+    where, R, C = "dsmoe_q8_quantize", int(R), int(C)
+    p, s = _take(where, handle, stream, x=(x, "bf16", R * C), q=(q, "q8", R * C),
+                 scales=(scales, "q8", R * dsmoe_q8_scale_cols(C)))
+    _check(_lib.dsmoe_q8_quantize(handle, R, C, *p, s), where)
+
+
+def dsmoe_q8_quantize_weights(handle, E, N, K, W, q, scales, stream=None) -> None:
+    where, E, N, K = "dsmoe_q8_quantize_weights", int(E), int(N), int(K)
+    p, s = _take(where, handle, stream, W=(W, "bf16", E * N * K), q=(q, "q8", E * N * K),
+                 scales=(scales, "q8", E * -(-N // 128) * dsmoe_q8_scale_cols(K)))
+    _check(_lib.dsmoe_q8_quantize_weights(handle, E, N, K, *p, s), where)
+
+
+def dsmoe_norm_q8(handle, T, x, residual, w, eps, r, u, q, scales, stream=None) -> None:
+    where, T = "dsmoe_norm_q8", int(T)
+    d = _norm_width(where, handle, w)
+    n = T * d
+    (x, residual, w, r, u, q, scales), s = _take(
+        where, handle, stream, x=(x, "bf16", n), residual=(residual, "bf16", n), w=(w, "bf16", d), r=(r, "bf16", n),
+        u=(u, "bf16", n), q=(q, "q8", n), scales=(scales, "q8", T * dsmoe_q8_scale_cols(d)))
+    _check(_lib.dsmoe_norm_q8(handle, T, x, residual, w, float(eps), r, u, q, scales, s), where)
+
+
+def dsmoe_norm_backward(handle, T, dy, dres, r, w, eps, dx, dw, stream=None) -> None:
+    where, T = "dsmoe_norm_backward", int(T)
+    d = _norm_width(where, handle, w)
+    n = T * d
+    (dy, dres, r, w, dx, dw), s = _take(where, handle, stream, dy=(dy, "f32", n), dres=(dres, "bf16", n), r=(r, "bf16", n),
+                                        w=(w, "bf16", d), dx=(dx, "bf16", n), dw=(dw, "f32", d))
+    _check(_lib.dsmoe_norm_backward(handle, T, dy, dres, r, w, float(eps), dx, dw, s), where)
+
+
+def dsmoe_q8_matmul(handle, E, R, N, K, offsets, a, a_scales, W, W_scales, out, stream=None) -> None:
+    where, E, R, N, K = "dsmoe_q8_matmul", int(E), int(R), int(N), int(K)
+    S = dsmoe_q8_scale_cols(K)
+    p, s = _take(where, handle, stream, offsets=(offsets, "i32", E + 1), a=(a, "q8", R * K), a_scales=(a_scales, "q8", R * S),
+                 W=(W, "q8", E * N * K), W_scales=(W_scales, "q8", E * -(-N // 128) * S), out=(out, "bf16", R * N))
+    _check(_lib.dsmoe_q8_matmul(handle, E, R, N, K, *p, s), where)
+
+
+def dsmoe_q8_gated_matmul(handle, E, R, N, K, offsets, a, a_scales, W_gate, gate_scales, W_up, up_scales, q, scales,
+                          stream=None) -> None:
+    where, E, R, N, K = "dsmoe_q8_gated_matmul", int(E), int(R), int(N), int(K)
+    S = dsmoe_q8_scale_cols(K)
+    nw, ns = E * N * K, E * -(-N // 128) * S
+    p, s = _take(where, handle, stream, offsets=(offsets, "i32", E + 1), a=(a, "q8", R * K), a_scales=(a_scales, "q8", R * S),
+                 W_gate=(W_gate, "q8", nw), gate_scales=(gate_scales, "q8", ns), W_up=(W_up, "q8", nw),
+                 up_scales=(up_scales, "q8", ns), q=(q, "q8", R * N), scales=(scales, "q8", R * dsmoe_q8_scale_cols(N)))
+    _check(_lib.dsmoe_q8_gated_matmul(handle, E, R, N, K, *p, s), where)
 
 
 _WS_DTYPES = {"logits": "float32", "offsets": "int32", "slot_of": "int32", "Xp": "bfloat16",

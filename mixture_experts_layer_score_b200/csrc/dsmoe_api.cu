@@ -14,11 +14,13 @@
 
 #include <algorithm>
 #include <functional>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 
 #include "dsmoe.h"
 #include "kernels.h"
+#include "q8.cuh"
 #include "role_clock.cuh"
 
 #define DSMOE_EXPORT extern "C" __attribute__((visibility("default")))
@@ -155,7 +157,7 @@ struct DeviceGuard {
 };
 
 struct Layout {
-  size_t logits, counts_ws, cursor, offsets, P_part, slot_of, Xp, A1, A1s, Y, Hs, status, seq_terms;
+  size_t logits, counts_ws, cursor, offsets, P_part, slot_of, Xp, A1, A1s, Y, Hs, status, seq_terms, norm_part;
   size_t x_stage[2], ids_stage[2], h_stage[2], topk_stage[2], gates_stage[2], counts_stage[2], f_stage[2],
       P_stage[2];  // two staging slots for the host entry points
   size_t total;
@@ -193,6 +195,8 @@ Layout plan(const dsmoe_cfg& c) {
   L.Hs = take(c.n_shared > 0 ? T * d * 4 : 0);
   L.status = take(4);
   L.seq_terms = take(T * 4);
+  L.norm_part = take(static_cast<size_t>(dsmoe::norm_backward_blocks(c.max_tokens, c.d_model, dsmoe::kNormMaxSms)) *
+                     d * 4);
   for (int i = 0; i < 2; ++i) {
     L.x_stage[i] = take(T * d * 2);
     L.ids_stage[i] = take(hash ? T * 4 : 0);
@@ -243,6 +247,7 @@ struct dsmoe_handle {
   float* Hs;
   uint32_t* status;
   float* seq_terms;
+  float* norm_part;  // dsmoe_norm_backward's per-block shares of dw
   struct Stage {
     bf16 *x, *h;
     int32_t *ids, *topk, *counts;
@@ -410,6 +415,7 @@ DSMOE_EXPORT dsmoe_status dsmoe_create(const dsmoe_cfg* cfg, int32_t device, dsm
   h->Hs = reinterpret_cast<float*>(w + L.Hs);
   h->status = reinterpret_cast<uint32_t*>(w + L.status);
   h->seq_terms = reinterpret_cast<float*>(w + L.seq_terms);
+  h->norm_part = reinterpret_cast<float*>(w + L.norm_part);
   for (int i = 0; i < 2; ++i) {
     h->stage[i].x = reinterpret_cast<bf16*>(w + L.x_stage[i]);
     h->stage[i].ids = reinterpret_cast<int32_t*>(w + L.ids_stage[i]);
@@ -1821,4 +1827,181 @@ DSMOE_EXPORT dsmoe_status dsmoe_bias_update(dsmoe_handle* h, int64_t T, const in
                                      static_cast<cudaStream_t>(stream)));
   h->launches += 1;
   return DSMOE_OK;
+}
+
+// ========================================================================================
+// the 8-bit path: block quantisation, the norm in front of the layer, grouped products
+// ========================================================================================
+namespace {
+// Every pointer of a call that has work: present and 16-byte aligned.
+dsmoe_status check_pointers(std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs) {
+    if (!p) return fail(DSMOE_ERR_INVALID_ARG, "NULL argument");
+    if (!aligned16(p)) return fail(DSMOE_ERR_INVALID_ARG, "pointer %p is not 16-byte aligned", p);
+  }
+  return DSMOE_OK;
+}
+
+constexpr int kQ8MaxDim = 32768;       // as d_model and d_ff
+constexpr int64_t kQ8MaxRows = 1 << 30;  // as max_tokens * top_k
+
+dsmoe_status check_q8_dims(int64_t R, int32_t E, int32_t N, int32_t K, int n_step) {
+  if (R < 0 || E < 1 || N < 1 || K < 1)
+    return fail(DSMOE_ERR_INVALID_ARG, "sizes must be positive (rows %lld, experts %d, N %d, K %d)",
+                static_cast<long long>(R), E, N, K);
+  if (R > kQ8MaxRows || E > 512 || N > kQ8MaxDim || K > kQ8MaxDim)
+    return fail(DSMOE_ERR_UNSUPPORTED, "rows %lld above 2^30, experts %d above 512, or N %d / K %d above 32768",
+                static_cast<long long>(R), E, N, K);
+  if (K % 16 || N % n_step)
+    return fail(DSMOE_ERR_UNSUPPORTED, "K = %d must be a multiple of 16 and N = %d of %d", K, N, n_step);
+  return DSMOE_OK;
+}
+
+dsmoe_status q8_matmul(dsmoe_handle* h, int32_t E, int64_t R, int32_t N, int32_t K, const int32_t* offsets,
+                       const void* a, const void* a_scales, const void* W, const void* W_scales, const void* W1,
+                       const void* W1_scales, void* out, void* q_out, void* q_scales, cudaStream_t s) {
+  dsmoe::Q8GemmArgs g;
+  memset(&g, 0, sizeof(g));
+  g.a = static_cast<const uint8_t*>(a);
+  g.a_scales = static_cast<const uint8_t*>(a_scales);
+  g.W = static_cast<const uint8_t*>(W);
+  g.W_scales = static_cast<const uint8_t*>(W_scales);
+  g.W1 = static_cast<const uint8_t*>(W1);
+  g.W1_scales = static_cast<const uint8_t*>(W1_scales);
+  g.offsets = offsets;
+  g.E = E;
+  g.R = static_cast<int>(R);
+  g.N = N;
+  g.K = K;
+  g.out = static_cast<bf16*>(out);
+  g.q_out = static_cast<uint8_t*>(q_out);
+  g.q_scales = static_cast<uint8_t*>(q_scales);
+  g.status = h->status;
+  CUDA_TRY(dsmoe::launch_q8_simple(g, s));
+  h->launches += 1;
+  return DSMOE_OK;
+}
+}  // namespace
+
+DSMOE_EXPORT int32_t dsmoe_q8_scale_cols(int32_t C) { return C > 0 ? dsmoe::q8_scale_cols(C) : 0; }
+
+DSMOE_EXPORT dsmoe_status dsmoe_q8_quantize(dsmoe_handle* h, int64_t R, int32_t C, const void* x, void* q,
+                                            void* scales, void* stream) {
+  if (!h) return fail(DSMOE_ERR_INVALID_ARG, "handle is NULL");
+  STAGE_TRY(check_q8_dims(R, 1, 1, C, 1));
+  if (R == 0) return DSMOE_OK;
+  STAGE_TRY(check_pointers({x, q, scales}));
+  DeviceGuard g(h->device);
+  if (!g.ok) return fail(DSMOE_ERR_CUDA, "cannot select device %d", h->device);
+  CUDA_TRY(dsmoe::launch_quantize_rows(static_cast<const bf16*>(x), R, C, static_cast<uint8_t*>(q),
+                                       static_cast<uint8_t*>(scales), h->num_sms, static_cast<cudaStream_t>(stream)));
+  h->launches += 1;
+  return DSMOE_OK;
+}
+
+DSMOE_EXPORT dsmoe_status dsmoe_q8_quantize_weights(dsmoe_handle* h, int32_t E, int32_t N, int32_t K, const void* W,
+                                                    void* q, void* scales, void* stream) {
+  if (!h) return fail(DSMOE_ERR_INVALID_ARG, "handle is NULL");
+  STAGE_TRY(check_q8_dims(0, E, N, K, 1));
+  STAGE_TRY(check_pointers({W, q, scales}));
+  DeviceGuard g(h->device);
+  if (!g.ok) return fail(DSMOE_ERR_CUDA, "cannot select device %d", h->device);
+  CUDA_TRY(dsmoe::launch_quantize_weights(static_cast<const bf16*>(W), E, N, K, static_cast<uint8_t*>(q),
+                                          static_cast<uint8_t*>(scales), h->num_sms,
+                                          static_cast<cudaStream_t>(stream)));
+  h->launches += 1;
+  return DSMOE_OK;
+}
+
+DSMOE_EXPORT dsmoe_status dsmoe_norm_q8(dsmoe_handle* h, int32_t T, const void* x, const void* residual,
+                                        const void* w, float eps, void* r, void* u, void* q, void* scales,
+                                        void* stream) {
+  if (!h) return fail(DSMOE_ERR_INVALID_ARG, "handle is NULL");
+  if (T < 0) return fail(DSMOE_ERR_INVALID_ARG, "T = %d is negative", T);
+  if (T > h->cfg.max_tokens) return fail(DSMOE_ERR_WORKSPACE, "T = %d exceeds max_tokens = %d", T, h->cfg.max_tokens);
+  if (!(eps >= 0.0f) || eps > 1e30f) return fail(DSMOE_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if ((q == nullptr) != (scales == nullptr)) return fail(DSMOE_ERR_INVALID_ARG, "q and scales come together");
+  if (!u && !q) return fail(DSMOE_ERR_INVALID_ARG, "u or q is required");
+  if (T == 0) return DSMOE_OK;
+  STAGE_TRY(check_pointers({x, w}));
+  for (const void* p : {residual, static_cast<const void*>(r), static_cast<const void*>(u),
+                        static_cast<const void*>(q), static_cast<const void*>(scales)})
+    if (p && !aligned16(p)) return fail(DSMOE_ERR_INVALID_ARG, "pointer %p is not 16-byte aligned", p);
+  DeviceGuard g(h->device);
+  if (!g.ok) return fail(DSMOE_ERR_CUDA, "cannot select device %d", h->device);
+  dsmoe::NormArgs a;
+  a.x = static_cast<const bf16*>(x);
+  a.residual = static_cast<const bf16*>(residual);
+  a.w = static_cast<const bf16*>(w);
+  a.eps = eps;
+  a.T = T;
+  a.d = h->cfg.d_model;
+  a.r = static_cast<bf16*>(r);
+  a.u = static_cast<bf16*>(u);
+  a.q = static_cast<uint8_t*>(q);
+  a.scales = static_cast<uint8_t*>(scales);
+  CUDA_TRY(dsmoe::launch_norm_q8(a, h->num_sms, static_cast<cudaStream_t>(stream)));
+  h->launches += 1;
+  return DSMOE_OK;
+}
+
+DSMOE_EXPORT dsmoe_status dsmoe_norm_backward(dsmoe_handle* h, int32_t T, const float* dy, const void* dres,
+                                              const void* r, const void* w, float eps, void* dx, float* dw,
+                                              void* stream) {
+  if (!h) return fail(DSMOE_ERR_INVALID_ARG, "handle is NULL");
+  if (T < 0) return fail(DSMOE_ERR_INVALID_ARG, "T = %d is negative", T);
+  if (T > h->cfg.max_tokens) return fail(DSMOE_ERR_WORKSPACE, "T = %d exceeds max_tokens = %d", T, h->cfg.max_tokens);
+  if (!(eps >= 0.0f) || eps > 1e30f) return fail(DSMOE_ERR_INVALID_ARG, "eps must be finite and not negative");
+  STAGE_TRY(check_pointers({dw}));
+  if (T > 0) STAGE_TRY(check_pointers({dy, r, w, dx}));
+  if (dres && !aligned16(dres)) return fail(DSMOE_ERR_INVALID_ARG, "pointer %p is not 16-byte aligned", dres);
+  DeviceGuard g(h->device);
+  if (!g.ok) return fail(DSMOE_ERR_CUDA, "cannot select device %d", h->device);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    CUDA_TRY(cudaMemsetAsync(dw, 0, static_cast<size_t>(h->cfg.d_model) * sizeof(float), s));
+    return DSMOE_OK;
+  }
+  dsmoe::NormBwdArgs a;
+  a.dy = dy;
+  a.dres = static_cast<const bf16*>(dres);
+  a.r = static_cast<const bf16*>(r);
+  a.w = static_cast<const bf16*>(w);
+  a.eps = eps;
+  a.T = T;
+  a.d = h->cfg.d_model;
+  a.dx = static_cast<bf16*>(dx);
+  a.part = h->norm_part;
+  CUDA_TRY(dsmoe::launch_norm_backward(a, dw, h->num_sms, s));
+  h->launches += 2;
+  return DSMOE_OK;
+}
+
+DSMOE_EXPORT dsmoe_status dsmoe_q8_matmul(dsmoe_handle* h, int32_t E, int64_t R, int32_t N, int32_t K,
+                                          const int32_t* offsets, const void* a, const void* a_scales, const void* W,
+                                          const void* W_scales, void* out, void* stream) {
+  if (!h) return fail(DSMOE_ERR_INVALID_ARG, "handle is NULL");
+  STAGE_TRY(check_q8_dims(R, E, N, K, 8));
+  if (!offsets) return fail(DSMOE_ERR_INVALID_ARG, "offsets is required");
+  if (R == 0) return DSMOE_OK;
+  STAGE_TRY(check_pointers({a, a_scales, W, W_scales, out}));
+  DeviceGuard g(h->device);
+  if (!g.ok) return fail(DSMOE_ERR_CUDA, "cannot select device %d", h->device);
+  return q8_matmul(h, E, R, N, K, offsets, a, a_scales, W, W_scales, nullptr, nullptr, out, nullptr, nullptr,
+                   static_cast<cudaStream_t>(stream));
+}
+
+DSMOE_EXPORT dsmoe_status dsmoe_q8_gated_matmul(dsmoe_handle* h, int32_t E, int64_t R, int32_t N, int32_t K,
+                                                const int32_t* offsets, const void* a, const void* a_scales,
+                                                const void* W_gate, const void* gate_scales, const void* W_up,
+                                                const void* up_scales, void* q, void* scales, void* stream) {
+  if (!h) return fail(DSMOE_ERR_INVALID_ARG, "handle is NULL");
+  STAGE_TRY(check_q8_dims(R, E, N, K, 16));
+  if (!offsets) return fail(DSMOE_ERR_INVALID_ARG, "offsets is required");
+  if (R == 0) return DSMOE_OK;
+  STAGE_TRY(check_pointers({a, a_scales, W_gate, gate_scales, W_up, up_scales, q, scales}));
+  DeviceGuard g(h->device);
+  if (!g.ok) return fail(DSMOE_ERR_CUDA, "cannot select device %d", h->device);
+  return q8_matmul(h, E, R, N, K, offsets, a, a_scales, W_gate, gate_scales, W_up, up_scales, nullptr, q, scales,
+                   static_cast<cudaStream_t>(stream));
 }

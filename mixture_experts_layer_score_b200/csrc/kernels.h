@@ -300,6 +300,61 @@ cudaError_t launch_down_pair(const GemmArgs& a, int clusters, cudaStream_t s);
 int gateup_pair_max_clusters();
 cudaError_t launch_gateup_pair(const GemmArgs& a, int clusters, cudaStream_t s);
 
+// ---------------------------------------------------------------- 8-bit path (q8.cu, q8.cuh)
+// q [R, C] e4m3 and scales [R, q8_scale_cols(C)] of the bf16 rows x (C a multiple of 16);
+// q [E, N, K] and scales [E, ceil(N / 128), q8_scale_cols(K)] of the weights W.
+cudaError_t launch_quantize_rows(const bf16* x, int64_t R, int C, uint8_t* q, uint8_t* scales, int num_sms,
+                                 cudaStream_t s);
+cudaError_t launch_quantize_weights(const bf16* W, int E, int N, int K, uint8_t* q, uint8_t* scales, int num_sms,
+                                    cudaStream_t s);
+
+// r = bf16(x + residual) (x without one), u = bf16(r rsqrt(mean(r^2) + eps) w), q8 of u.
+struct NormArgs {
+  const bf16* x;
+  const bf16* residual;  // or nullptr
+  const bf16* w;         // [d]
+  float eps;
+  int T, d;
+  bf16* r;               // or nullptr
+  bf16* u;               // or nullptr
+  uint8_t* q;            // or nullptr, then scales is too
+  uint8_t* scales;
+};
+cudaError_t launch_norm_q8(const NormArgs& a, int num_sms, cudaStream_t s);
+// dx = dres + the norm's gradient of dy at r, and dw; part holds one row of d floats per block.
+struct NormBwdArgs {
+  const float* dy;
+  const bf16* dres;  // or nullptr
+  const bf16* r;
+  const bf16* w;
+  float eps;
+  int T, d;
+  bf16* dx;
+  float* part;       // [norm_backward_blocks, d]
+};
+constexpr int kNormMaxSms = 192;  // SMs that the partial sums are sized for
+int norm_backward_blocks(int64_t T, int d, int num_sms);
+cudaError_t launch_norm_backward(const NormBwdArgs& a, float* dw, int num_sms, cudaStream_t s);
+
+// Grouped products of 8-bit rows with 8-bit weights: rows offsets[e] .. offsets[e+1] of a
+// [R, K] times expert e's W [N, K]. One weight: out = the product in bf16. Two (W1 set):
+// SiLU(a W^T) (a W1^T) in 8 bits (q_out, q_scales).
+struct Q8GemmArgs {
+  const uint8_t* a;
+  const uint8_t* a_scales;   // [R, q8_scale_cols(K)]
+  const uint8_t* W;
+  const uint8_t* W_scales;   // [E, ceil(N / 128), q8_scale_cols(K)]
+  const uint8_t* W1;
+  const uint8_t* W1_scales;
+  const int32_t* offsets;    // [E + 1]
+  int E, R, N, K;
+  bf16* out;                 // [R, N]
+  uint8_t* q_out;            // [R, N]
+  uint8_t* q_scales;         // [R, q8_scale_cols(N)]
+  uint32_t* status;
+};
+cudaError_t launch_q8_simple(const Q8GemmArgs& a, cudaStream_t s);
+
 // ---------------------------------------------------------------- errors (dsmoe_api.cu)
 // Record the calling thread's last-error message (read back by dsmoe_last_error).
 void note_error(const char* fmt, ...);
