@@ -100,6 +100,21 @@ bool map_3d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t rows, uint
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Byte map of a [rows, inner] or (three) [outer, rows, inner] tensor,
+// 128-byte swizzle, box (128, box_rows): the 8-bit products' operands.
+bool map_bytes(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t rows, uint64_t outer, uint32_t box_rows,
+               bool three = false) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {inner, rows, outer};
+  cuuint64_t strides[2] = {inner, inner * rows};
+  cuuint32_t box[3] = {128, box_rows, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, three ? 3 : 2, const_cast<void*>(ptr), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 4D bf16 view (64, rows, cols / 64, experts) of an [experts, rows, cols] tensor whose
 // cols are contiguous, 128-byte swizzle, box (64, 64, 4, 1): one copy lands 256 cols x 64
 // rows as four MN-major atoms (the backward GEMMs' A operand).
@@ -1862,11 +1877,12 @@ dsmoe_status q8_matmul(dsmoe_handle* h, int32_t E, int64_t R, int32_t N, int32_t
                        const void* W1_scales, void* out, void* q_out, void* q_scales, cudaStream_t s) {
   dsmoe::Q8GemmArgs g;
   memset(&g, 0, sizeof(g));
-  g.a = static_cast<const uint8_t*>(a);
+  const int tok = dsmoe::q8_token_tile(R, E, K);
+  if (!map_bytes(&g.map_a, a, K, R, 1, tok) || !map_bytes(&g.map_w0, W, K, N, E, 128, true) ||
+      !map_bytes(&g.map_w1, W1 ? W1 : W, K, N, E, 128, true))
+    return fail(DSMOE_ERR_CUDA, "cuTensorMapEncodeTiled rejected a tensor map of this call");
   g.a_scales = static_cast<const uint8_t*>(a_scales);
-  g.W = static_cast<const uint8_t*>(W);
   g.W_scales = static_cast<const uint8_t*>(W_scales);
-  g.W1 = static_cast<const uint8_t*>(W1);
   g.W1_scales = static_cast<const uint8_t*>(W1_scales);
   g.offsets = offsets;
   g.E = E;
@@ -1877,7 +1893,8 @@ dsmoe_status q8_matmul(dsmoe_handle* h, int32_t E, int64_t R, int32_t N, int32_t
   g.q_out = static_cast<uint8_t*>(q_out);
   g.q_scales = static_cast<uint8_t*>(q_scales);
   g.status = h->status;
-  CUDA_TRY(dsmoe::launch_q8_simple(g, s));
+  g.wait_limit_ns = h->wait_ns;
+  CUDA_TRY(dsmoe::launch_gemm_q8(g, tok, h->num_sms, s));
   h->launches += 1;
   return DSMOE_OK;
 }

@@ -1,0 +1,549 @@
+// gemm_q8_sm100.cu -- persistent grouped products of 8-bit rows with 8-bit expert weights on
+// the 5th-generation tensor cores (tcgen05 kind::mxf8f6f4, block-scaled), operands staged by
+// TMA, scales copied from shared into tensor memory.
+//
+//   out[r, n] = sum_b 2^(sa[r,b] + sw[n/128,b] - 254) sum_{k in block b} a[r,k] W[e,n,k]
+//
+// The scales are powers of two, so the tensor core applies them itself (one e8m0 byte per
+// 32 values of K; a block of 128 uses the same byte for its four MMAs) and the fp32
+// accumulator in tensor memory holds the scaled sum over all of K: no partial sum is ever
+// read back to be rescaled.
+//
+// Orientation as in the bf16 grouped GEMM (gemm_sm100.cu): M = 128 output features per chain,
+// N = the tile's tokens rounded up to 16, two chains sharing the token operand (gated: the
+// same 128 features of W_gate and W_up; plain: 256 consecutive features).
+//
+// One CTA per SM, 352 threads:
+//   warp 0      TMA producer: per 128-wide K block two 128 x 128 weight tiles and a
+//               kTok x 128 token tile (bytes, 128-byte swizzle) through a ring.
+//   warp 1      one thread issues, per four K blocks, the copies of the scales into tensor
+//               memory (32x128b.warpx4) and, per K block, 2 x 4 MMAs of K = 32.
+//   warps 2-9   epilogue: two groups of four warps take alternate 16-token chunks; warp q of
+//               a group reads TMEM lanes [32q, 32q+32), the group transposes the chunk
+//               through shared memory so that each output row leaves in one coalesced
+//               store. 128 features are one scale block, so the gated output's maximum over
+//               a block is a maximum over the row of the staged chunk.
+//   warp 10     scale loader: a 32-bit word of a row's scales is four K blocks; the words
+//               of the tile's tokens and of the two weight tiles go to a ring of slots
+//               in the layout that the copy into tensor memory takes.
+// Every wait is bounded; a role that gives up raises the abort flag and a status bit, the
+// CTA drains its copies and MMAs and returns. The epilogue's groups decide together
+// (through shared memory), so that none of their barriers is left waiting.
+#include "kernels.h"
+#include "q8.cuh"
+#include "sm100_ptx.cuh"
+
+namespace dsmoe {
+
+namespace {
+
+constexpr int kBK = 128;    // K per ring stage: one 128-byte swizzled row, one scale block
+constexpr int kFeat = 128;  // features per chain
+constexpr int kMmaK = 32;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (2 + kEpiWarps + 1);
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kWBytes = 2 * kFeat * kBK;
+constexpr int kSfSlots = 4;
+constexpr uint32_t kSfCols = 16;        // TMEM columns of one set: 4 + 4 (weights), 8 (tokens)
+constexpr uint32_t kSfCol0 = kTmemCols - 2 * kSfCols;
+constexpr int kChunk = 16;              // tokens per epilogue chunk
+constexpr uint32_t kStgBytes = kChunk * kFeat * 4;
+
+enum { kOutBf16 = 0, kOutGated = 1, kOutF32 = 2 };
+
+template <int kTok>
+struct Geo {
+  static constexpr uint32_t kAccCols = 2 * kTok;
+  static constexpr int kBufs = 2 * kAccCols <= kSfCol0 ? 2 : 1;
+  static constexpr int kStages = kTok > 112 ? 3 : kTok > 32 ? 4 : 5;
+  static constexpr uint32_t kXBytes = kTok * kBK;
+  static constexpr uint32_t kStageBytes = kWBytes + kXBytes;
+  static constexpr uint32_t kSfBytes = kTok > 128 ? 2048 : 1536;  // weight tiles 2 x 512, tokens 512 or 1024
+  static constexpr uint32_t kOffW = 0;
+  static constexpr uint32_t kOffX = kOffW + kStages * kWBytes;
+  static constexpr uint32_t kOffSf = kOffX + kStages * kXBytes;
+  static constexpr uint32_t kOffStg = kOffSf + kSfSlots * kSfBytes;
+  static constexpr uint32_t kOffBars = kOffStg + 4 * kStgBytes;  // two groups, two buffers
+  static constexpr uint32_t kNumBars = 2 * kStages + 2 * kSfSlots + 4 + 1;
+  static constexpr uint32_t kOffMisc = kOffBars + kNumBars * 8;
+  static constexpr uint32_t kOffTiles = kOffMisc + 32;
+  static constexpr uint32_t kSmemUsed = kOffTiles + (512 + 1) * 4;
+  static constexpr size_t kSmemBytes = kSmemUsed + 1024;  // slack to align the ring to 1024 bytes
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+  static_assert(kAccCols <= kSfCol0 && kTok % 16 == 0 && kTok <= 256, "tile geometry");
+  static_assert(kXBytes % 1024 == 0, "token tiles start on swizzle atoms");
+};
+
+// D[tmem] (+)= (A 2^sfa)(B 2^sfb)^T, e4m3 operands, e8m0 scales in tensor memory.
+__device__ __forceinline__ void mma_q8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}\n" ::"r"(
+          d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+      : "memory");
+}
+
+// Instruction descriptor of kind::mxf8f6f4: e4m3 A and B (format codes 0), e8m0 scales (bit
+// 23), K-major, byte `id` of each 32-bit word of scales for both operands.
+__device__ __forceinline__ uint32_t idesc_q8(int m, int n, uint32_t id) {
+  return (id << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) | (static_cast<uint32_t>(m >> 4) << 24) |
+         (id << 29);
+}
+
+// 512 bytes of shared memory (32 rows of 16 bytes) into four columns, the same for each
+// quarter of the lanes: row i's word j is the scales of operand row i + 32 j.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t saddr) {
+  uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(1) << 16;         // leading byte offset (one 16-byte column: unused)
+  d |= static_cast<uint64_t>(128 >> 4) << 32;  // stride byte offset: next eight rows
+  d |= static_cast<uint64_t>(1) << 46;         // descriptor version for sm_100
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void group_sync(int half) {
+  asm volatile("bar.sync %0, %1;" ::"r"(half + 1), "r"(128) : "memory");
+}
+
+struct Q8Tile {
+  int expert, row0, m_valid, n_blk;
+};
+
+// Rows [b, t) of group e: offsets clipped to [0, R], empty where they decrease.
+__device__ __forceinline__ void group_rows(const Q8GemmArgs& a, int e, int& b, int& t) {
+  b = min(max(__ldg(a.offsets + e), 0), a.R);
+  t = max(min(max(__ldg(a.offsets + e + 1), 0), a.R), b);
+}
+
+template <int kTok>
+__device__ __forceinline__ Q8Tile decode_tile(const Q8GemmArgs& a, const int32_t* tile_start, int tile) {
+  int lo = 0, hi = a.E - 1;
+  while (lo < hi) {  // last group whose first tile is <= tile
+    const int mid = (lo + hi + 1) >> 1;
+    if (tile_start[mid] <= tile) lo = mid;
+    else hi = mid - 1;
+  }
+  int b, e;
+  group_rows(a, lo, b, e);
+  const int M = e - b, mt = (M + kTok - 1) / kTok, local = tile - tile_start[lo], m_blk = local % mt;
+  // near-equal token tiles in granules of 16, token tiles fastest: the CTAs that share a
+  // weight tile run at the same rate and find it in L2
+  const int gr = (M + 15) >> 4, q = gr / mt, rem = gr - q * mt;
+  const int g0 = m_blk * q + min(m_blk, rem);
+  Q8Tile t;
+  t.expert = lo;
+  t.n_blk = local / mt;
+  t.row0 = b + g0 * 16;
+  t.m_valid = min((q + (m_blk < rem ? 1 : 0)) * 16, M - g0 * 16);
+  return t;
+}
+
+template <int kOut, int kTok>
+__global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_constant__ Q8GemmArgs a) {
+  using G_ = Geo<kTok>;
+  constexpr bool kGated = kOut == kOutGated;
+  constexpr int kTileFeat = kGated ? kFeat : 2 * kFeat;  // output features of a tile
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
+  uint8_t* base = smem_raw + pad;
+  uint8_t* sW = base + G_::kOffW;
+  uint8_t* sX = base + G_::kOffX;
+  uint8_t* sSf = base + G_::kOffSf;
+  uint64_t* full = reinterpret_cast<uint64_t*>(base + G_::kOffBars);
+  uint64_t* empty = full + G_::kStages;
+  uint64_t* sf_full = empty + G_::kStages;
+  uint64_t* sf_empty = sf_full + kSfSlots;
+  uint64_t* acc_full = sf_empty + kSfSlots;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + G_::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(base + G_::kOffMisc + 4);
+  volatile int* never_flag = reinterpret_cast<volatile int*>(base + G_::kOffMisc + 8);
+  volatile int* group_ok = reinterpret_cast<volatile int*>(base + G_::kOffMisc + 16);  // [epilogue group][tile parity]
+  int32_t* tile_start = reinterpret_cast<int32_t*>(base + G_::kOffTiles);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n_tiles = (a.N + kTileFeat - 1) / kTileFeat;
+  const int kb_n = (a.K + kBK - 1) / kBK, kq_n = (kb_n + 3) >> 2;
+
+  for (int e = threadIdx.x; e < a.E; e += kThreads) {
+    int b, t;
+    group_rows(a, e, b, t);
+    tile_start[e + 1] = ((t - b + kTok - 1) / kTok) * n_tiles;
+  }
+  if (threadIdx.x == 0) {
+    tile_start[0] = 0;
+    *abort_flag = 0;
+    *never_flag = 0;
+    for (int s = 0; s < G_::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < kSfSlots; ++s) {
+      mbar_init(&sf_full[s], 32);
+      mbar_init(&sf_empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  if (warp == 0) {  // inclusive prefix over tile_start[1..E]
+    int carry = 0;
+    for (int b0 = 1; b0 <= a.E; b0 += 32) {
+      const int i = b0 + lane;
+      int v = (i <= a.E) ? tile_start[i] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int n = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += n;
+      }
+      if (i <= a.E) tile_start[i] = v + carry;
+      carry += __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int total = tile_start[a.E];
+
+  uint32_t issued_mask = 0, issued_parity = 0;  // producer bookkeeping for the abort drain
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------------ TMA producer
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+        const Q8Tile t = decode_tile<kTok>(a, tile_start, tile);
+        const int n0 = t.n_blk * kTileFeat;
+        for (int kb = 0; kb < kb_n; ++kb) {
+          if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, a.wait_limit_ns, abort_flag)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full[stage], G_::kStageBytes);
+          uint8_t* w = sW + stage * kWBytes;
+          tma_load_3d(w, &a.map_w0, &full[stage], kb * kBK, n0, t.expert);
+          tma_load_3d(w + kWBytes / 2, kGated ? &a.map_w1 : &a.map_w0, &full[stage], kb * kBK,
+                      kGated ? n0 : n0 + kFeat, t.expert);
+          tma_load_2d(sX + stage * G_::kXBytes, &a.map_a, &full[stage], kb * kBK, t.row0);
+          issued_mask |= 1u << stage;
+          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == G_::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        *abort_flag = 1;
+        atomicOr(a.status, kStatusTimeoutProducer);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ------------------------------------------------------------------ MMA issuer
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t quad = 0;  // groups of four K blocks so far
+      bool ok = true;
+      int it = 0;
+      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x, ++it) {
+        const Q8Tile t = decode_tile<kTok>(a, tile_start, tile);
+        const int n_mma = (t.m_valid + 15) & ~15;
+        const uint32_t idesc = idesc_q8(kFeat, n_mma, 0);
+        const int acc = it % G_::kBufs;
+        if (!mbar_wait_bounded(&acc_empty[acc], ((it / G_::kBufs) & 1) ^ 1u, a.wait_limit_ns, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d0 = tmem_base + acc * G_::kAccCols;
+        uint32_t sf = 0;
+        for (int kb = 0; kb < kb_n; ++kb) {
+          const uint32_t id = kb & 3;
+          if (id == 0) {
+            // the columns of this set were last read by the MMAs of two groups ago
+            const uint32_t slot = quad % kSfSlots;
+            if ((quad >= 2 && !mbar_wait_bounded(&sf_empty[(quad - 2) % kSfSlots], ((quad - 2) / kSfSlots) & 1u,
+                                                 a.wait_limit_ns, abort_flag)) ||
+                !mbar_wait_bounded(&sf_full[slot], (quad / kSfSlots) & 1u, a.wait_limit_ns, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            sf = tmem_base + kSfCol0 + (quad & 1u) * kSfCols;
+            const uint32_t s0 = smem_addr(sSf + slot * G_::kSfBytes);
+            tmem_copy_scales(sf, s0);
+            tmem_copy_scales(sf + 4, s0 + 512);
+            tmem_copy_scales(sf + 8, s0 + 1024);
+            if (n_mma > 128) tmem_copy_scales(sf + 12, s0 + 1536);
+          }
+          if (!mbar_wait_bounded(&full[stage], phase, a.wait_limit_ns, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t w0 = smem_desc_kmajor_sw128(smem_addr(sW + stage * kWBytes));
+          const uint64_t w1 = smem_desc_kmajor_sw128(smem_addr(sW + stage * kWBytes + kWBytes / 2));
+          const uint64_t xd = smem_desc_kmajor_sw128(smem_addr(sX + stage * G_::kXBytes));
+          const uint32_t di = idesc | (id << 4) | (id << 29);
+#pragma unroll
+          for (int k = 0; k < kBK / kMmaK; ++k) {
+            const uint64_t dk = static_cast<uint64_t>(2 * k);
+            const uint32_t accum = (kb | k) ? 1u : 0u;
+            mma_q8_ss(d0, w0 + dk, xd + dk, di, sf, sf + 8, accum);
+            mma_q8_ss(d0 + kTok, w1 + dk, xd + dk, di, sf + 4, sf + 8, accum);
+          }
+          mma_commit(&empty[stage]);
+          if (id == 3 || kb == kb_n - 1) {
+            mma_commit(&sf_empty[quad % kSfSlots]);
+            ++quad;
+          }
+          if (++stage == G_::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        mma_commit(&acc_full[acc]);
+      }
+      if (!ok) {
+        *abort_flag = 1;
+        atomicOr(a.status, kStatusTimeoutMma);
+      }
+    }
+  } else if (warp == 2 + kEpiWarps) {
+    // -------------------------------------------------------------------- scale loader
+    const int S4 = q8_scale_cols(a.K) >> 2, nnb = (a.N + kFeat - 1) / kFeat;
+    const uint32_t* as = reinterpret_cast<const uint32_t*>(a.a_scales);
+    const uint32_t* ws0 = reinterpret_cast<const uint32_t*>(a.W_scales);
+    const uint32_t* ws1 = reinterpret_cast<const uint32_t*>(kGated ? a.W1_scales : a.W_scales);
+    constexpr uint32_t kOnes = 0x7F7F7F7Fu;
+    constexpr int kWords = (kTok + 31) / 32;
+    uint32_t quad = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+      const Q8Tile t = decode_tile<kTok>(a, tile_start, tile);
+      const int nb0 = kGated ? t.n_blk : 2 * t.n_blk, nb1 = kGated ? nb0 : nb0 + 1;
+      const uint32_t* p0 = ws0 + (static_cast<int64_t>(t.expert) * nnb + nb0) * S4;
+      const uint32_t* p1 = ws1 + (static_cast<int64_t>(t.expert) * nnb + nb1) * S4;
+      uint32_t w[8], g0, g1;
+      auto load = [&](int kq) {
+        g0 = __ldg(p0 + kq);
+        g1 = nb1 < nnb ? __ldg(p1 + kq) : kOnes;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          w[i] = kOnes;
+          if (i < kWords && 32 * i + lane < t.m_valid)
+            w[i] = __ldg(as + static_cast<int64_t>(t.row0 + 32 * i + lane) * S4 + kq);
+        }
+      };
+      load(0);
+      for (int kq = 0; kq < kq_n; ++kq, ++quad) {
+        const uint32_t slot = quad % kSfSlots;
+        if (!mbar_wait_warp(&sf_empty[slot], ((quad / kSfSlots) & 1u) ^ 1u, a.wait_limit_ns, abort_flag)) {
+          ok = false;
+          break;
+        }
+        uint4* dst = reinterpret_cast<uint4*>(sSf + slot * G_::kSfBytes) + lane;
+        dst[0] = make_uint4(g0, g0, g0, g0);
+        dst[32] = make_uint4(g1, g1, g1, g1);
+        dst[64] = make_uint4(w[0], w[1], w[2], w[3]);
+        if (kTok > 128) dst[96] = make_uint4(w[4], w[5], w[6], w[7]);
+        fence_proxy_async();
+        mbar_arrive(&sf_full[slot]);
+        if (kq + 1 < kq_n) load(kq + 1);
+      }
+    }
+    if (!ok && lane == 0) {
+      *abort_flag = 1;
+      atomicOr(a.status, kStatusTimeoutProducer);
+    }
+  } else {
+    // -------------------------------------------------------------------- epilogue
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const bool leader = ((warp - 2) & 3) == 0 && lane == 0;
+    uint8_t* stg = base + G_::kOffStg + half * 2 * kStgBytes;
+    uint32_t buf = 0;  // staging buffer of the next chunk
+    const int So = kGated ? q8_scale_cols(a.N) : 0, nbo = (a.N + kFeat - 1) / kFeat;
+    const int w4 = (warp - 2) & 3;  // this warp's rows of a staged chunk: 4 w4 .. 4 w4 + 3
+    int it = 0;
+    for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++it) {
+      const Q8Tile t = decode_tile<kTok>(a, tile_start, tile);
+      const int acc = it % G_::kBufs;
+      if (leader) {
+        const bool ok = mbar_wait_bounded(&acc_full[acc], (it / G_::kBufs) & 1, a.wait_limit_ns, abort_flag);
+        group_ok[2 * half + (it & 1)] = ok;
+        if (!ok) {
+          *abort_flag = 1;
+          atomicOr(a.status, kStatusTimeoutEpilogue);
+        }
+      }
+      group_sync(half);
+      // the same answer for the whole group (its warps are at most one tile apart)
+      if (!group_ok[2 * half + (it & 1)]) break;
+      (void)mbar_try_wait(&acc_full[acc], (it / G_::kBufs) & 1);
+      tc_fence_after();
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * G_::kAccCols;
+      const int n_chunks = (t.m_valid + kChunk - 1) / kChunk;
+      const int n0 = t.n_blk * kTileFeat;
+      uint32_t v0[16], v1[16];
+      if (half < n_chunks) {
+        tmem_ld16(tb + kChunk * half, v0);
+        tmem_ld16(tb + kTok + kChunk * half, v1);
+      }
+#pragma unroll 1
+      for (int c = half; c < n_chunks; c += 2) {
+        tmem_wait_ld();
+        const bool more = c + 2 < n_chunks;
+        const uint32_t cn = static_cast<uint32_t>(kChunk * (c + 2));
+        if (kGated) {
+          float* st = reinterpret_cast<float*>(stg + buf * kStgBytes);
+#pragma unroll
+          for (int j = 0; j < kChunk; ++j) {
+            const float g = __uint_as_float(v0[j]);
+            st[j * kFeat + q * 32 + lane] = __fdividef(g, 1.0f + __expf(-g)) * __uint_as_float(v1[j]);
+          }
+        } else if (kOut == kOutBf16) {
+          uint16_t* st = reinterpret_cast<uint16_t*>(stg + buf * kStgBytes);
+#pragma unroll
+          for (int j = 0; j < kChunk; ++j) {
+            st[j * 2 * kFeat + q * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v0[j])));
+            st[j * 2 * kFeat + kFeat + q * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v1[j])));
+          }
+        } else {  // fp32: chain 0 now, chain 1 through the other buffer below
+          float* st = reinterpret_cast<float*>(stg + buf * kStgBytes);
+          float* st1 = reinterpret_cast<float*>(stg + (buf ^ 1u) * kStgBytes);
+          group_sync(half);  // both buffers are free
+#pragma unroll
+          for (int j = 0; j < kChunk; ++j) {
+            st[j * kFeat + q * 32 + lane] = __uint_as_float(v0[j]);
+            st1[j * kFeat + q * 32 + lane] = __uint_as_float(v1[j]);
+          }
+        }
+        if (more) {
+          tmem_ld16(tb + cn, v0);
+          tmem_ld16(tb + kTok + cn, v1);
+        }
+        group_sync(half);
+        // rows of the chunk, four per warp, each in one coalesced store
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = 4 * w4 + i, tok = c * kChunk + j;
+          if (tok >= t.m_valid) break;
+          const int64_t row = t.row0 + tok;
+          if (kGated) {
+            const float4 m = reinterpret_cast<const float4*>(stg + buf * kStgBytes)[j * (kFeat / 4) + lane];
+            const uint32_t mx = __reduce_max_sync(0xffffffffu, max(max(abs_bits(m.x), abs_bits(m.y)),
+                                                                   max(abs_bits(m.z), abs_bits(m.w))));
+            const uint32_t s = q8_scale_byte(mx);
+            const float k = q8_inv_scale(s);
+            const int f = n0 + 4 * lane;
+            if (f < a.N)
+              *reinterpret_cast<uint32_t*>(a.q_out + row * a.N + f) =
+                  s == 255u ? 0x7F7F7F7Fu : q8_pack4(m.x * k, m.y * k, m.z * k, m.w * k);
+            if (lane == 0) a.q_scales[row * So + t.n_blk] = static_cast<uint8_t>(s);
+            if (t.n_blk == nbo - 1 && lane < So - nbo) a.q_scales[row * So + nbo + lane] = kQ8PadScale;
+          } else if (kOut == kOutBf16) {
+            const uint4 o = reinterpret_cast<const uint4*>(stg + buf * kStgBytes)[j * (2 * kFeat / 8) + lane];
+            const int f = n0 + 8 * lane;
+            if (f < a.N) *reinterpret_cast<uint4*>(a.out + row * a.N + f) = o;
+          } else {
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch) {
+              float4 o = reinterpret_cast<const float4*>(stg + (buf ^ ch) * kStgBytes)[j * (kFeat / 4) + lane];
+              const int f = n0 + ch * kFeat + 4 * lane;
+              if (f < a.N) {
+                const int64_t at = row * a.N + f;
+                if (a.add_bf16) {
+                  const uint2 r = *reinterpret_cast<const uint2*>(a.add_bf16 + at);
+                  const float2 r0 = unpack_bf16x2(r.x), r1 = unpack_bf16x2(r.y);
+                  o.x += r0.x, o.y += r0.y, o.z += r1.x, o.w += r1.y;
+                } else {
+                  const float4 r = *reinterpret_cast<const float4*>(a.out_f32 + at);
+                  o.x += r.x, o.y += r.y, o.z += r.z, o.w += r.w;
+                }
+                *reinterpret_cast<float4*>(a.out_f32 + at) = o;
+              }
+            }
+          }
+        }
+        if (kOut != kOutF32) buf ^= 1u;
+      }
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[acc]);
+    }
+  }
+
+  __syncthreads();
+  if (*abort_flag) {
+    // let every copy and MMA this CTA started finish before its memory is released
+    if (warp == 0 && lane == 0) {
+      for (int s = 0; s < G_::kStages; ++s)
+        if ((issued_mask >> s) & 1u)
+          if (!mbar_wait_bounded(&full[s], (issued_parity >> s) & 1u, drain_wait_limit(a.wait_limit_ns), never_flag))
+            atomicOr(a.status, kStatusTimeoutDrain);
+    }
+    if (warp == 1 && lane == 0) {
+      mma_commit(drain);
+      if (!mbar_wait_bounded(drain, 0, drain_wait_limit(a.wait_limit_ns), never_flag))
+        atomicOr(a.status, kStatusTimeoutDrain);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kTmemCols);
+  }
+}
+
+template <int kOut, int kTok>
+cudaError_t launch_one(const Q8GemmArgs& a, int grid, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(gemm_q8_kernel<kOut, kTok>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(Geo<kTok>::kSmemBytes));
+  if (e != cudaSuccess) return e;
+  gemm_q8_kernel<kOut, kTok><<<grid, kThreads, Geo<kTok>::kSmemBytes, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <int kOut>
+cudaError_t launch_tok(const Q8GemmArgs& a, int tok, int grid, cudaStream_t s) {
+  if (tok == 32) return launch_one<kOut, 32>(a, grid, s);
+  if (tok == 112) return launch_one<kOut, 112>(a, grid, s);
+  return launch_one<kOut, 224>(a, grid, s);
+}
+}  // namespace
+
+int q8_token_tile(int64_t R, int E, int K) {
+  if (R <= 24LL * E) return 32;
+  return R >= 160LL * E && K >= 1024 ? 224 : 112;
+}
+
+cudaError_t launch_gemm_q8(const Q8GemmArgs& a, int tok, int num_sms, cudaStream_t s) {
+  const bool gated = a.q_out != nullptr;
+  const int64_t n_tiles = (a.N + (gated ? 127 : 255)) / (gated ? 128 : 256);
+  const int64_t bound = ((a.R + tok - 1) / tok + a.E) * n_tiles;
+  const int grid = static_cast<int>(bound < num_sms ? bound : num_sms);
+  if (gated) return launch_tok<kOutGated>(a, tok, grid, s);
+  return a.out_f32 ? launch_tok<kOutF32>(a, tok, grid, s) : launch_tok<kOutBf16>(a, tok, grid, s);
+}
+
+}  // namespace dsmoe

@@ -336,24 +336,30 @@ constexpr int kNormMaxSms = 192;  // SMs that the partial sums are sized for
 int norm_backward_blocks(int64_t T, int d, int num_sms);
 cudaError_t launch_norm_backward(const NormBwdArgs& a, float* dw, int num_sms, cudaStream_t s);
 
-// Grouped products of 8-bit rows with 8-bit weights: rows offsets[e] .. offsets[e+1] of a
-// [R, K] times expert e's W [N, K]. One weight: out = the product in bf16. Two (W1 set):
-// SiLU(a W^T) (a W1^T) in 8 bits (q_out, q_scales).
+// Grouped products of 8-bit rows with 8-bit weights (gemm_q8_sm100.cu): rows offsets[e] ..
+// offsets[e+1] of a [R, K] times expert e's W [N, K]. One of three outputs: `out` bf16;
+// q_out, q_scales: SiLU(a W^T) (a W1^T) in 8 bits; out_f32 fp32, added to add_bf16 or, without
+// it, to what out_f32 holds.
 struct Q8GemmArgs {
-  const uint8_t* a;
+  CUtensorMap map_a;         // 2D [R, K] bytes, box (128, token tile)
+  CUtensorMap map_w0;        // 3D (K, N, experts) bytes, box (128, 128): W (gated: W_gate)
+  CUtensorMap map_w1;        // gated: W_up
   const uint8_t* a_scales;   // [R, q8_scale_cols(K)]
-  const uint8_t* W;
   const uint8_t* W_scales;   // [E, ceil(N / 128), q8_scale_cols(K)]
-  const uint8_t* W1;
   const uint8_t* W1_scales;
   const int32_t* offsets;    // [E + 1]
   int E, R, N, K;
   bf16* out;                 // [R, N]
   uint8_t* q_out;            // [R, N]
   uint8_t* q_scales;         // [R, q8_scale_cols(N)]
+  float* out_f32;            // [R, N]
+  const bf16* add_bf16;      // [R, N] or nullptr
   uint32_t* status;
+  uint64_t wait_limit_ns;
 };
-cudaError_t launch_q8_simple(const Q8GemmArgs& a, cudaStream_t s);
+// Tokens per tile (the row box of map_a) for R rows over E groups.
+int q8_token_tile(int64_t R, int E, int K);
+cudaError_t launch_gemm_q8(const Q8GemmArgs& a, int tok, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- errors (dsmoe_api.cu)
 // Record the calling thread's last-error message (read back by dsmoe_last_error).
