@@ -1878,7 +1878,7 @@ dsmoe_status q8_matmul(dsmoe_handle* h, int32_t E, int64_t R, int32_t N, int32_t
   dsmoe::Q8GemmArgs g;
   memset(&g, 0, sizeof(g));
   const int tok = dsmoe::q8_token_tile(R, E, K);
-  if (!map_bytes(&g.map_a, a, K, R, 1, tok) || !map_bytes(&g.map_w0, W, K, N, E, 128, true) ||
+  if (!map_bytes(&g.map_a, a, K, R, 1, dsmoe::q8_box_rows(tok)) || !map_bytes(&g.map_w0, W, K, N, E, 128, true) ||
       !map_bytes(&g.map_w1, W1 ? W1 : W, K, N, E, 128, true))
     return fail(DSMOE_ERR_CUDA, "cuTensorMapEncodeTiled rejected a tensor map of this call");
   g.a_scales = static_cast<const uint8_t*>(a_scales);

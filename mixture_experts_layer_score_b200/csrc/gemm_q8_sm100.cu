@@ -18,10 +18,10 @@
 //               kTok x 128 token tile (bytes, 128-byte swizzle) through a ring.
 //   warp 1      one thread issues, per four K blocks, the copies of the scales into tensor
 //               memory (32x128b.warpx4) and, per K block, 2 x 4 MMAs of K = 32.
-//   warps 2-9   epilogue: two groups of four warps take alternate 16-token chunks; warp q of
-//               a group reads TMEM lanes [32q, 32q+32), the group transposes the chunk
-//               through shared memory so that each output row leaves in one coalesced
-//               store. 128 features are one scale block, so the gated output's maximum over
+//   warps 2-9   epilogue: two groups of four warps take alternate 8-token chunks; warp q of
+//               a group reads TMEM lanes [32q, 32q+32) into registers and frees the
+//               accumulator; the group then transposes two chunks at a time through shared
+//               memory so that each output row leaves in one coalesced store. 128 features are one scale block, so the gated output's maximum over
 //               a block is a maximum over the row of the staged chunk.
 //   warp 10     scale loader: a 32-bit word of a row's scales is four K blocks; the words
 //               of the tile's tokens and of the two weight tiles go to a ring of slots
@@ -44,11 +44,11 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kEpiWarps + 1);
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kWBytes = 2 * kFeat * kBK;
-constexpr int kSfSlots = 4;
+constexpr int kSfSlots = 2;
 constexpr uint32_t kSfCols = 16;        // TMEM columns of one set: 4 + 4 (weights), 8 (tokens)
 constexpr uint32_t kSfCol0 = kTmemCols - 2 * kSfCols;
-constexpr int kChunk = 16;              // tokens per epilogue chunk
-constexpr uint32_t kStgBytes = kChunk * kFeat * 4;
+constexpr int kChunk = 8;               // tokens per epilogue chunk
+constexpr uint32_t kStgBytes = 2 * kChunk * kFeat * 4;
 
 enum { kOutBf16 = 0, kOutGated = 1, kOutF32 = 2 };
 
@@ -58,7 +58,7 @@ struct Geo {
   static constexpr int kBufs = 2 * kAccCols <= kSfCol0 ? 2 : 1;
   static constexpr int kStages = kTok > 112 ? 3 : kTok > 32 ? 4 : 5;
   static constexpr uint32_t kXBytes = kTok * kBK;
-  static constexpr uint32_t kStageBytes = kWBytes + kXBytes;
+  static constexpr uint32_t kBoxRows = q8_box_rows(kTok);
   static constexpr uint32_t kSfBytes = kTok > 128 ? 2048 : 1536;  // weight tiles 2 x 512, tokens 512 or 1024
   static constexpr uint32_t kOffW = 0;
   static constexpr uint32_t kOffX = kOffW + kStages * kWBytes;
@@ -72,7 +72,8 @@ struct Geo {
   static constexpr size_t kSmemBytes = kSmemUsed + 1024;  // slack to align the ring to 1024 bytes
   static_assert(kSmemBytes <= 232448, "shared memory budget");
   static_assert(kAccCols <= kSfCol0 && kTok % 16 == 0 && kTok <= 256, "tile geometry");
-  static_assert(kXBytes % 1024 == 0, "token tiles start on swizzle atoms");
+  static_assert(kXBytes % 1024 == 0 && kTok % kBoxRows == 0 && kBoxRows % 8 == 0,
+                "token boxes start on swizzle atoms");
 };
 
 // D[tmem] (+)= (A 2^sfa)(B 2^sfb)^T, e4m3 operands, e8m0 scales in tensor memory.
@@ -94,6 +95,12 @@ __device__ __forceinline__ uint32_t idesc_q8(int m, int n, uint32_t id) {
          (id << 29);
 }
 
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
 // 512 bytes of shared memory (32 rows of 16 bytes) into four columns, the same for each
 // quarter of the lanes: row i's word j is the scales of operand row i + 32 j.
 __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t saddr) {
@@ -107,6 +114,28 @@ __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t saddr)
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void group_sync(int half) {
   asm volatile("bar.sync %0, %1;" ::"r"(half + 1), "r"(128) : "memory");
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, e;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
+// mbar_wait_bounded for a converged warp: every lane polls, the decisions are the warp's.
+__device__ __forceinline__ bool mbar_wait_converged(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
+                                                    volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if ((i & 63u) == 0 && __any_sync(0xffffffffu, *abort_flag != 0 || global_timer_ns() - t0 > limit_ns)) return false;
+  }
 }
 
 struct Q8Tile {
@@ -147,6 +176,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
   using G_ = Geo<kTok>;
   constexpr bool kGated = kOut == kOutGated;
   constexpr int kTileFeat = kGated ? kFeat : 2 * kFeat;  // output features of a tile
+  constexpr int kHold = (kTok / kChunk + 1) / 2;         // chunks of an epilogue group
+  static_assert(kOut != kOutF32 || kTok <= 112, "the fp32 output holds both chains in registers");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
   uint8_t* base = smem_raw + pad;
@@ -230,17 +261,23 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
       for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
         const Q8Tile t = decode_tile<kTok>(a, tile_start, tile);
         const int n0 = t.n_blk * kTileFeat;
+        // only the boxes that hold rows of the tile: the copies into shared memory are what
+        // bounds the large products
+        const int boxes = (t.m_valid + G_::kBoxRows - 1) / G_::kBoxRows;
+        const uint32_t stage_bytes = kWBytes + boxes * G_::kBoxRows * kBK;
         for (int kb = 0; kb < kb_n; ++kb) {
           if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, a.wait_limit_ns, abort_flag)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&full[stage], G_::kStageBytes);
+          mbar_arrive_expect_tx(&full[stage], stage_bytes);
           uint8_t* w = sW + stage * kWBytes;
           tma_load_3d(w, &a.map_w0, &full[stage], kb * kBK, n0, t.expert);
           tma_load_3d(w + kWBytes / 2, kGated ? &a.map_w1 : &a.map_w0, &full[stage], kb * kBK,
                       kGated ? n0 : n0 + kFeat, t.expert);
-          tma_load_2d(sX + stage * G_::kXBytes, &a.map_a, &full[stage], kb * kBK, t.row0);
+          for (int i = 0; i < boxes; ++i)
+            tma_load_2d(sX + stage * G_::kXBytes + i * G_::kBoxRows * kBK, &a.map_a, &full[stage], kb * kBK,
+                        t.row0 + i * static_cast<int>(G_::kBoxRows));
           issued_mask |= 1u << stage;
           issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
           if (++stage == G_::kStages) {
@@ -255,53 +292,59 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ------------------------------------------------------------------ MMA issuer
-      int stage = 0;
-      uint32_t phase = 0;
-      uint32_t quad = 0;  // groups of four K blocks so far
-      bool ok = true;
-      int it = 0;
-      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x, ++it) {
-        const Q8Tile t = decode_tile<kTok>(a, tile_start, tile);
-        const int n_mma = (t.m_valid + 15) & ~15;
-        const uint32_t idesc = idesc_q8(kFeat, n_mma, 0);
-        const int acc = it % G_::kBufs;
-        if (!mbar_wait_bounded(&acc_empty[acc], ((it / G_::kBufs) & 1) ^ 1u, a.wait_limit_ns, abort_flag)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d0 = tmem_base + acc * G_::kAccCols;
-        uint32_t sf = 0;
-        for (int kb = 0; kb < kb_n; ++kb) {
-          const uint32_t id = kb & 3;
-          if (id == 0) {
-            // the columns of this set were last read by the MMAs of two groups ago
-            const uint32_t slot = quad % kSfSlots;
-            if ((quad >= 2 && !mbar_wait_bounded(&sf_empty[(quad - 2) % kSfSlots], ((quad - 2) / kSfSlots) & 1u,
+    // -------------------------------------------------------------------- MMA issuer
+    // The whole warp walks the loop and one elected lane issues, so that the descriptors stay
+    // in uniform registers: issued from a branch on the lane number, eight MMAs took
+    // 950 cycles whatever their N (N = 128 needs 512).
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t quad = 0;  // groups of four K blocks so far
+    bool ok = true;
+    int it = 0;
+    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x, ++it) {
+      const Q8Tile t = decode_tile<kTok>(a, tile_start, tile);
+      const int n_mma = (t.m_valid + 15) & ~15;
+      const uint32_t idesc = idesc_q8(kFeat, n_mma, 0);
+      const int acc = it % G_::kBufs;
+      if (!mbar_wait_converged(&acc_empty[acc], ((it / G_::kBufs) & 1) ^ 1u, a.wait_limit_ns, abort_flag)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d0 = tmem_base + acc * G_::kAccCols;
+      uint32_t sf = 0;
+      for (int kb = 0; kb < kb_n; ++kb) {
+        const uint32_t id = kb & 3;
+        if (id == 0) {
+          // the columns of this set were last read by the MMAs of two groups ago
+          const uint32_t slot = quad % kSfSlots;
+          if ((quad >= 2 && !mbar_wait_converged(&sf_empty[(quad - 2) % kSfSlots], ((quad - 2) / kSfSlots) & 1u,
                                                  a.wait_limit_ns, abort_flag)) ||
-                !mbar_wait_bounded(&sf_full[slot], (quad / kSfSlots) & 1u, a.wait_limit_ns, abort_flag)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            sf = tmem_base + kSfCol0 + (quad & 1u) * kSfCols;
-            const uint32_t s0 = smem_addr(sSf + slot * G_::kSfBytes);
+              !mbar_wait_converged(&sf_full[slot], (quad / kSfSlots) & 1u, a.wait_limit_ns, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          sf = tmem_base + kSfCol0 + (quad & 1u) * kSfCols;
+          const uint32_t s0 = smem_addr(sSf + slot * G_::kSfBytes);
+          if (elect_one()) {
             tmem_copy_scales(sf, s0);
             tmem_copy_scales(sf + 4, s0 + 512);
             tmem_copy_scales(sf + 8, s0 + 1024);
             if (n_mma > 128) tmem_copy_scales(sf + 12, s0 + 1536);
           }
-          if (!mbar_wait_bounded(&full[stage], phase, a.wait_limit_ns, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t w0 = smem_desc_kmajor_sw128(smem_addr(sW + stage * kWBytes));
-          const uint64_t w1 = smem_desc_kmajor_sw128(smem_addr(sW + stage * kWBytes + kWBytes / 2));
-          const uint64_t xd = smem_desc_kmajor_sw128(smem_addr(sX + stage * G_::kXBytes));
-          const uint32_t di = idesc | (id << 4) | (id << 29);
+          __syncwarp();
+        }
+        if (!mbar_wait_converged(&full[stage], phase, a.wait_limit_ns, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t w0 = smem_desc_kmajor_sw128(smem_addr(sW + stage * kWBytes));
+        const uint64_t w1 = smem_desc_kmajor_sw128(smem_addr(sW + stage * kWBytes + kWBytes / 2));
+        const uint64_t xd = smem_desc_kmajor_sw128(smem_addr(sX + stage * G_::kXBytes));
+        const uint32_t di = idesc | (id << 4) | (id << 29);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kBK / kMmaK; ++k) {
             const uint64_t dk = static_cast<uint64_t>(2 * k);
@@ -310,22 +353,20 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
             mma_q8_ss(d0 + kTok, w1 + dk, xd + dk, di, sf + 4, sf + 8, accum);
           }
           mma_commit(&empty[stage]);
-          if (id == 3 || kb == kb_n - 1) {
-            mma_commit(&sf_empty[quad % kSfSlots]);
-            ++quad;
-          }
-          if (++stage == G_::kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          if (id == 3 || kb == kb_n - 1) mma_commit(&sf_empty[quad % kSfSlots]);
+          if (kb == kb_n - 1) mma_commit(&acc_full[acc]);
         }
-        if (!ok) break;
-        mma_commit(&acc_full[acc]);
+        __syncwarp();
+        if (id == 3 || kb == kb_n - 1) ++quad;
+        if (++stage == G_::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      if (!ok) {
-        *abort_flag = 1;
-        atomicOr(a.status, kStatusTimeoutMma);
-      }
+    }
+    if (!ok && lane == 0) {
+      *abort_flag = 1;
+      atomicOr(a.status, kStatusTimeoutMma);
     }
   } else if (warp == 2 + kEpiWarps) {
     // -------------------------------------------------------------------- scale loader
@@ -402,53 +443,70 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * G_::kAccCols;
       const int n_chunks = (t.m_valid + kChunk - 1) / kChunk;
       const int n0 = t.n_blk * kTileFeat;
-      uint32_t v0[16], v1[16];
+      // First the accumulators move to registers (gated: through SwiGLU; bf16: both chains
+      // rounded into one register), so that the next tile's MMAs may overwrite them ...
+      uint32_t hold[kHold][kChunk], hold1[kOut == kOutF32 ? kHold : 1][kChunk];
+      uint32_t v0[2][kChunk], v1[2][kChunk];
       if (half < n_chunks) {
-        tmem_ld16(tb + kChunk * half, v0);
-        tmem_ld16(tb + kTok + kChunk * half, v1);
+        tmem_ld8(tb + kChunk * half, v0[0]);
+        tmem_ld8(tb + kTok + kChunk * half, v1[0]);
       }
-#pragma unroll 1
-      for (int c = half; c < n_chunks; c += 2) {
+#pragma unroll
+      for (int i = 0; i < kHold; ++i) {
+        const int c = 2 * i + half;
+        if (c >= n_chunks) break;
         tmem_wait_ld();
-        const bool more = c + 2 < n_chunks;
-        const uint32_t cn = static_cast<uint32_t>(kChunk * (c + 2));
-        if (kGated) {
-          float* st = reinterpret_cast<float*>(stg + buf * kStgBytes);
+        if (i + 1 < kHold && c + 2 < n_chunks) {
+          tmem_ld8(tb + kChunk * (c + 2), v0[(i + 1) & 1]);
+          tmem_ld8(tb + kTok + kChunk * (c + 2), v1[(i + 1) & 1]);
+        }
 #pragma unroll
-          for (int j = 0; j < kChunk; ++j) {
-            const float g = __uint_as_float(v0[j]);
-            st[j * kFeat + q * 32 + lane] = __fdividef(g, 1.0f + __expf(-g)) * __uint_as_float(v1[j]);
-          }
-        } else if (kOut == kOutBf16) {
-          uint16_t* st = reinterpret_cast<uint16_t*>(stg + buf * kStgBytes);
-#pragma unroll
-          for (int j = 0; j < kChunk; ++j) {
-            st[j * 2 * kFeat + q * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v0[j])));
-            st[j * 2 * kFeat + kFeat + q * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v1[j])));
-          }
-        } else {  // fp32: chain 0 now, chain 1 through the other buffer below
-          float* st = reinterpret_cast<float*>(stg + buf * kStgBytes);
-          float* st1 = reinterpret_cast<float*>(stg + (buf ^ 1u) * kStgBytes);
-          group_sync(half);  // both buffers are free
-#pragma unroll
-          for (int j = 0; j < kChunk; ++j) {
-            st[j * kFeat + q * 32 + lane] = __uint_as_float(v0[j]);
-            st1[j * kFeat + q * 32 + lane] = __uint_as_float(v1[j]);
+        for (int j = 0; j < kChunk; ++j) {
+          const float x = __uint_as_float(v0[i & 1][j]), y = __uint_as_float(v1[i & 1][j]);
+          if (kGated) hold[i][j] = __float_as_uint(__fdividef(x, 1.0f + __expf(-x)) * y);
+          else if (kOut == kOutBf16) hold[i][j] = pack_bf16x2(x, y);
+          else {
+            hold[i][j] = v0[i & 1][j];
+            hold1[kOut == kOutF32 ? i : 0][j] = v1[i & 1][j];
           }
         }
-        if (more) {
-          tmem_ld16(tb + cn, v0);
-          tmem_ld16(tb + kTok + cn, v1);
+      }
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[acc]);
+      // ... then two chunks at a time are transposed through shared memory and leave row by
+      // row, four rows per warp.
+#pragma unroll
+      for (int i = 0; i < kHold; i += 2) {
+        if (2 * i + half >= n_chunks) break;
+        float* st = reinterpret_cast<float*>(stg + buf * kStgBytes);
+        float* st1 = reinterpret_cast<float*>(stg + (buf ^ 1u) * kStgBytes);
+        uint16_t* sh = reinterpret_cast<uint16_t*>(st);
+        if (kOut == kOutF32) group_sync(half);  // both buffers are free
+#pragma unroll
+        for (int j = 0; j < 2 * kChunk; ++j) {
+          const int ii = i + (j >= kChunk ? 1 : 0);
+          if (ii >= kHold) break;
+          const uint32_t v = hold[ii][j & (kChunk - 1)];
+          if (kGated) st[j * kFeat + q * 32 + lane] = __uint_as_float(v);
+          else if (kOut == kOutBf16) {
+            sh[j * 2 * kFeat + q * 32 + lane] = static_cast<uint16_t>(v);
+            sh[j * 2 * kFeat + kFeat + q * 32 + lane] = static_cast<uint16_t>(v >> 16);
+          } else {
+            st[j * kFeat + q * 32 + lane] = __uint_as_float(v);
+            st1[j * kFeat + q * 32 + lane] = __uint_as_float(hold1[kOut == kOutF32 ? ii : 0][j & (kChunk - 1)]);
+          }
         }
         group_sync(half);
-        // rows of the chunk, four per warp, each in one coalesced store
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int j = 4 * w4 + i, tok = c * kChunk + j;
+        for (int r = 0; r < 4; ++r) {
+          const int j = 4 * w4 + r;
+          const int tok = kChunk * (2 * (i + (j >= kChunk ? 1 : 0)) + half) + (j & (kChunk - 1));
           if (tok >= t.m_valid) break;
           const int64_t row = t.row0 + tok;
           if (kGated) {
-            const float4 m = reinterpret_cast<const float4*>(stg + buf * kStgBytes)[j * (kFeat / 4) + lane];
+            const float4 m = reinterpret_cast<const float4*>(st)[j * (kFeat / 4) + lane];
             const uint32_t mx = __reduce_max_sync(0xffffffffu, max(max(abs_bits(m.x), abs_bits(m.y)),
                                                                    max(abs_bits(m.z), abs_bits(m.w))));
             const uint32_t s = q8_scale_byte(mx);
@@ -460,23 +518,23 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
             if (lane == 0) a.q_scales[row * So + t.n_blk] = static_cast<uint8_t>(s);
             if (t.n_blk == nbo - 1 && lane < So - nbo) a.q_scales[row * So + nbo + lane] = kQ8PadScale;
           } else if (kOut == kOutBf16) {
-            const uint4 o = reinterpret_cast<const uint4*>(stg + buf * kStgBytes)[j * (2 * kFeat / 8) + lane];
+            const uint4 o = reinterpret_cast<const uint4*>(sh)[j * (2 * kFeat / 8) + lane];
             const int f = n0 + 8 * lane;
             if (f < a.N) *reinterpret_cast<uint4*>(a.out + row * a.N + f) = o;
           } else {
 #pragma unroll
             for (int ch = 0; ch < 2; ++ch) {
-              float4 o = reinterpret_cast<const float4*>(stg + (buf ^ ch) * kStgBytes)[j * (kFeat / 4) + lane];
+              float4 o = reinterpret_cast<const float4*>(ch ? st1 : st)[j * (kFeat / 4) + lane];
               const int f = n0 + ch * kFeat + 4 * lane;
               if (f < a.N) {
                 const int64_t at = row * a.N + f;
                 if (a.add_bf16) {
-                  const uint2 r = *reinterpret_cast<const uint2*>(a.add_bf16 + at);
-                  const float2 r0 = unpack_bf16x2(r.x), r1 = unpack_bf16x2(r.y);
-                  o.x += r0.x, o.y += r0.y, o.z += r1.x, o.w += r1.y;
+                  const uint2 x = *reinterpret_cast<const uint2*>(a.add_bf16 + at);
+                  const float2 x0 = unpack_bf16x2(x.x), x1 = unpack_bf16x2(x.y);
+                  o.x += x0.x, o.y += x0.y, o.z += x1.x, o.w += x1.y;
                 } else {
-                  const float4 r = *reinterpret_cast<const float4*>(a.out_f32 + at);
-                  o.x += r.x, o.y += r.y, o.z += r.z, o.w += r.w;
+                  const float4 x = *reinterpret_cast<const float4*>(a.out_f32 + at);
+                  o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
                 }
                 *reinterpret_cast<float4*>(a.out_f32 + at) = o;
               }
@@ -485,10 +543,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
         }
         if (kOut != kOutF32) buf ^= 1u;
       }
-      tmem_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[acc]);
     }
   }
 
@@ -527,14 +581,15 @@ cudaError_t launch_one(const Q8GemmArgs& a, int grid, cudaStream_t s) {
 template <int kOut>
 cudaError_t launch_tok(const Q8GemmArgs& a, int tok, int grid, cudaStream_t s) {
   if (tok == 32) return launch_one<kOut, 32>(a, grid, s);
-  if (tok == 112) return launch_one<kOut, 112>(a, grid, s);
-  return launch_one<kOut, 224>(a, grid, s);
+  if constexpr (kOut != kOutF32)
+    if (tok == 240) return launch_one<kOut, 240>(a, grid, s);
+  return launch_one<kOut, 112>(a, grid, s);
 }
 }  // namespace
 
 int q8_token_tile(int64_t R, int E, int K) {
   if (R <= 24LL * E) return 32;
-  return R >= 160LL * E && K >= 1024 ? 224 : 112;
+  return R >= 160LL * E && K >= 1024 ? 240 : 112;
 }
 
 cudaError_t launch_gemm_q8(const Q8GemmArgs& a, int tok, int num_sms, cudaStream_t s) {

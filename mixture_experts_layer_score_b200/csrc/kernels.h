@@ -341,7 +341,7 @@ cudaError_t launch_norm_backward(const NormBwdArgs& a, float* dw, int num_sms, c
 // q_out, q_scales: SiLU(a W^T) (a W1^T) in 8 bits; out_f32 fp32, added to add_bf16 or, without
 // it, to what out_f32 holds.
 struct Q8GemmArgs {
-  CUtensorMap map_a;         // 2D [R, K] bytes, box (128, token tile)
+  CUtensorMap map_a;         // 2D [R, K] bytes, box (128, q8_box_rows(token tile))
   CUtensorMap map_w0;        // 3D (K, N, experts) bytes, box (128, 128): W (gated: W_gate)
   CUtensorMap map_w1;        // gated: W_up
   const uint8_t* a_scales;   // [R, q8_scale_cols(K)]
@@ -357,8 +357,10 @@ struct Q8GemmArgs {
   uint32_t* status;
   uint64_t wait_limit_ns;
 };
-// Tokens per tile (the row box of map_a) for R rows over E groups.
+// Tokens per tile for R rows over E groups, and the row box of map_a: a tile copies the
+// boxes that hold its rows.
 int q8_token_tile(int64_t R, int E, int K);
+constexpr int q8_box_rows(int tok) { return tok == 240 ? 48 : tok == 112 ? 56 : 16; }
 cudaError_t launch_gemm_q8(const Q8GemmArgs& a, int tok, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- errors (dsmoe_api.cu)
