@@ -401,33 +401,48 @@ def dsmoe_bias_update(handle, T, counts, alpha, b, stream=None):
 
 # ---- the 8-bit path. Byte tensors (e4m3 values, e8m0 scales) may be of any one-byte dtype, e.g.
 # torch.float8_e4m3fn and torch.float8_e8m0fnu.
-_BYTES = ("torch.float8_e4m3fn", "torch.float8_e8m0fnu", "torch.uint8", "torch.int8")
-_DTYPES = {"bf16": ("torch.bfloat16",), "f32": ("torch.float32",), "i32": ("torch.int32",), "q8": _BYTES}
+_DTYPES: Dict[str, tuple] = {}
 
 
-def _take(where: str, handle, stream, **tensors):
-    """Check the torch tensors of a call (name -> (tensor, kind, elements); raw addresses pass) and
+def _dtypes(kind: str) -> tuple:
+    if not _DTYPES:
+        import torch
+        _DTYPES.update(bf16=(torch.bfloat16,), f32=(torch.float32,), i32=(torch.int32,),
+                       q8=(torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.uint8, torch.int8))
+    return _DTYPES[kind]
+
+
+def _take(where: str, handle, stream, *tensors):
+    """Check the torch tensors of a call ((name, tensor, kind, elements); raw addresses pass) and
     return their addresses in order, and the stream: the caller's, or the current stream of
     the handle's device."""
     device = _handles[handle][0] if handle in _handles else None
+    kinds = _DTYPES or (_dtypes("bf16"), _DTYPES)[1]
     ptrs = []
-    for name, (t, kind, n) in tensors.items():
+    for name, t, kind, n in tensors:
         if t is None or isinstance(t, int):
             ptrs.append(t)
             continue
-        if str(t.dtype) not in _DTYPES[kind]:
-            raise DsmoeError(DSMOE_ERR_INVALID_ARG, where, f"{name} is {t.dtype}, not {' or '.join(_DTYPES[kind])}")
-        if t.numel() != n:
-            raise DsmoeError(DSMOE_ERR_INVALID_ARG, where, f"{name} has {t.numel()} elements, not {n}")
-        if not t.is_contiguous():
-            raise DsmoeError(DSMOE_ERR_INVALID_ARG, where, f"{name} is not contiguous")
-        if not t.is_cuda or (device is not None and t.device.index != device):
-            raise DsmoeError(DSMOE_ERR_INVALID_ARG, where, f"{name} is on {t.device}, not on the handle's GPU")
+        if t.dtype not in kinds[kind] or t.numel() != n or not t.is_contiguous() or \
+                (t.get_device() != device if device is not None else not t.is_cuda):
+            _refuse(where, name, t, kind, n)
         ptrs.append(t.data_ptr())
     if stream is None and device is not None:
         import torch
-        stream = torch.cuda.current_stream(device).cuda_stream
+        stream = torch._C._cuda_getCurrentRawStream(device)  # current_stream() without the Stream object
     return ptrs, _stream(stream)
+
+
+def _refuse(where: str, name: str, t, kind: str, n: int):
+    if t.dtype not in _dtypes(kind):
+        why = f"is {t.dtype}, not {' or '.join(map(str, _dtypes(kind)))}"
+    elif t.numel() != n:
+        why = f"has {t.numel()} elements, not {n}"
+    elif not t.is_contiguous():
+        why = "is not contiguous"
+    else:
+        why = f"is on {t.device}, not on the handle's GPU"
+    raise DsmoeError(DSMOE_ERR_INVALID_ARG, where, f"{name} {why}")
 
 
 def _norm_width(where, handle, w) -> int:
@@ -445,15 +460,15 @@ def dsmoe_q8_scale_cols(C: int) -> int:
 
 def dsmoe_q8_quantize(handle, R, C, x, q, scales, stream=None) -> None:
     where, R, C = "dsmoe_q8_quantize", int(R), int(C)
-    p, s = _take(where, handle, stream, x=(x, "bf16", R * C), q=(q, "q8", R * C),
-                 scales=(scales, "q8", R * dsmoe_q8_scale_cols(C)))
+    p, s = _take(where, handle, stream, ("x", x, "bf16", R * C), ("q", q, "q8", R * C),
+                 ("scales", scales, "q8", R * dsmoe_q8_scale_cols(C)))
     _check(_lib.dsmoe_q8_quantize(handle, R, C, *p, s), where)
 
 
 def dsmoe_q8_quantize_weights(handle, E, N, K, W, q, scales, stream=None) -> None:
     where, E, N, K = "dsmoe_q8_quantize_weights", int(E), int(N), int(K)
-    p, s = _take(where, handle, stream, W=(W, "bf16", E * N * K), q=(q, "q8", E * N * K),
-                 scales=(scales, "q8", E * -(-N // 128) * dsmoe_q8_scale_cols(K)))
+    p, s = _take(where, handle, stream, ("W", W, "bf16", E * N * K), ("q", q, "q8", E * N * K),
+                 ("scales", scales, "q8", E * -(-N // 128) * dsmoe_q8_scale_cols(K)))
     _check(_lib.dsmoe_q8_quantize_weights(handle, E, N, K, *p, s), where)
 
 
@@ -462,8 +477,8 @@ def dsmoe_norm_q8(handle, T, x, residual, w, eps, r, u, q, scales, stream=None) 
     d = _norm_width(where, handle, w)
     n = T * d
     (x, residual, w, r, u, q, scales), s = _take(
-        where, handle, stream, x=(x, "bf16", n), residual=(residual, "bf16", n), w=(w, "bf16", d), r=(r, "bf16", n),
-        u=(u, "bf16", n), q=(q, "q8", n), scales=(scales, "q8", T * dsmoe_q8_scale_cols(d)))
+        where, handle, stream, ("x", x, "bf16", n), ("residual", residual, "bf16", n), ("w", w, "bf16", d), ("r", r, "bf16", n),
+        ("u", u, "bf16", n), ("q", q, "q8", n), ("scales", scales, "q8", T * dsmoe_q8_scale_cols(d)))
     _check(_lib.dsmoe_norm_q8(handle, T, x, residual, w, float(eps), r, u, q, scales, s), where)
 
 
@@ -471,16 +486,16 @@ def dsmoe_norm_backward(handle, T, dy, dres, r, w, eps, dx, dw, stream=None) -> 
     where, T = "dsmoe_norm_backward", int(T)
     d = _norm_width(where, handle, w)
     n = T * d
-    (dy, dres, r, w, dx, dw), s = _take(where, handle, stream, dy=(dy, "f32", n), dres=(dres, "bf16", n), r=(r, "bf16", n),
-                                        w=(w, "bf16", d), dx=(dx, "bf16", n), dw=(dw, "f32", d))
+    (dy, dres, r, w, dx, dw), s = _take(where, handle, stream, ("dy", dy, "f32", n), ("dres", dres, "bf16", n), ("r", r, "bf16", n),
+                                        ("w", w, "bf16", d), ("dx", dx, "bf16", n), ("dw", dw, "f32", d))
     _check(_lib.dsmoe_norm_backward(handle, T, dy, dres, r, w, float(eps), dx, dw, s), where)
 
 
 def dsmoe_q8_matmul(handle, E, R, N, K, offsets, a, a_scales, W, W_scales, out, stream=None) -> None:
     where, E, R, N, K = "dsmoe_q8_matmul", int(E), int(R), int(N), int(K)
     S = dsmoe_q8_scale_cols(K)
-    p, s = _take(where, handle, stream, offsets=(offsets, "i32", E + 1), a=(a, "q8", R * K), a_scales=(a_scales, "q8", R * S),
-                 W=(W, "q8", E * N * K), W_scales=(W_scales, "q8", E * -(-N // 128) * S), out=(out, "bf16", R * N))
+    p, s = _take(where, handle, stream, ("offsets", offsets, "i32", E + 1), ("a", a, "q8", R * K), ("a_scales", a_scales, "q8", R * S),
+                 ("W", W, "q8", E * N * K), ("W_scales", W_scales, "q8", E * -(-N // 128) * S), ("out", out, "bf16", R * N))
     _check(_lib.dsmoe_q8_matmul(handle, E, R, N, K, *p, s), where)
 
 
@@ -489,9 +504,9 @@ def dsmoe_q8_gated_matmul(handle, E, R, N, K, offsets, a, a_scales, W_gate, gate
     where, E, R, N, K = "dsmoe_q8_gated_matmul", int(E), int(R), int(N), int(K)
     S = dsmoe_q8_scale_cols(K)
     nw, ns = E * N * K, E * -(-N // 128) * S
-    p, s = _take(where, handle, stream, offsets=(offsets, "i32", E + 1), a=(a, "q8", R * K), a_scales=(a_scales, "q8", R * S),
-                 W_gate=(W_gate, "q8", nw), gate_scales=(gate_scales, "q8", ns), W_up=(W_up, "q8", nw),
-                 up_scales=(up_scales, "q8", ns), q=(q, "q8", R * N), scales=(scales, "q8", R * dsmoe_q8_scale_cols(N)))
+    p, s = _take(where, handle, stream, ("offsets", offsets, "i32", E + 1), ("a", a, "q8", R * K), ("a_scales", a_scales, "q8", R * S),
+                 ("W_gate", W_gate, "q8", nw), ("gate_scales", gate_scales, "q8", ns), ("W_up", W_up, "q8", nw),
+                 ("up_scales", up_scales, "q8", ns), ("q", q, "q8", R * N), ("scales", scales, "q8", R * dsmoe_q8_scale_cols(N)))
     _check(_lib.dsmoe_q8_gated_matmul(handle, E, R, N, K, *p, s), where)
 
 

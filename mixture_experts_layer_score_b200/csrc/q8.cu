@@ -2,6 +2,8 @@
 // (1 x 128 blocks) and of expert weights (128 x 128), and the RMSNorm in front of the
 // layer, which adds the residual, writes the bf16 rows that the router reads and the 8-bit
 // rows that the experts read, with its backward pass.
+#include <algorithm>
+
 #include "kernels.h"
 #include "q8.cuh"
 #include "sm100_ptx.cuh"
@@ -70,7 +72,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const bf16* __restri
 
 // One block of threads per 128 x 128 tile of one expert's matrix; the tile stays in registers
 // between the maximum and the encoding (thread: eight columns of rows i, i + 16, ...).
-__global__ void __launch_bounds__(256) quantize_weights_kernel(const bf16* __restrict__ W, int64_t tiles, int N, int K,
+__global__ void __launch_bounds__(256, 4) quantize_weights_kernel(const bf16* __restrict__ W, int64_t tiles, int N, int K,
                                                                uint8_t* __restrict__ q,
                                                                uint8_t* __restrict__ scales) {
   __shared__ uint32_t s_max[8];
@@ -117,180 +119,289 @@ __global__ void __launch_bounds__(256) quantize_weights_kernel(const bf16* __res
   }
 }
 
-// Sum over the block in a fixed order (warp butterflies, then the warps' sums in order); every
-// thread gets the result. `red` holds 32 floats and is free again after the next call's
-// first barrier.
-__device__ __forceinline__ float block_sum(float v, float* red) {
+// Sums of n values over the block, in a fixed order (warp butterflies, then the warps' sums in
+// order); every thread gets them. red holds 32 n floats that the block has zeroed once; two
+// of them used in turn make one barrier per call enough.
+template <int n>
+__device__ __forceinline__ void block_sums(float (&v)[n], float* red) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int warps = blockDim.x >> 5;
+  for (int i = 0; i < n; ++i)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  const int warp = threadIdx.x >> 5;
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int i = 0; i < n; ++i) red[32 * i + warp] = v[i];
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float t = 0.f;
-  for (int i = 0; i < warps; ++i) t += red[i];
-  return t;
+  const int quads = (static_cast<int>(blockDim.x >> 5) + 3) >> 2;
+#pragma unroll
+  for (int i = 0; i < n; ++i) {
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j >= quads) break;
+      const float4 p = reinterpret_cast<const float4*>(red + 32 * i)[j];
+      s += (p.x + p.y) + (p.z + p.w);
+    }
+    v[i] = s;
+  }
 }
 
-// One row per block: r = bf16(x + residual) stays in registers (8 NV values per thread)
-// between the sum of squares and the scaled row u = bf16((r rstd) w); the 8-bit row is
-// that of u, so that it equals the quantisation of the bf16 row.
+__device__ __forceinline__ uint4 add_bf16x8(const uint4& a, const uint4& b) {
+  float x[8], y[8];
+  unpack8(a, x);
+  unpack8(b, y);
+  return make_uint4(pack_bf16x2(x[0] + y[0], x[1] + y[1]), pack_bf16x2(x[2] + y[2], x[3] + y[3]),
+                    pack_bf16x2(x[4] + y[4], x[5] + y[5]), pack_bf16x2(x[6] + y[6], x[7] + y[7]));
+}
+
+// One row at a time per block, 8 NV values per thread: r = bf16(x + residual) stays in
+// registers between the sum of squares and the scaled row u = bf16((r rstd) w); the 8-bit
+// row is that of u, so that it equals the quantisation of the bf16 row. The block loads
+// its next row before it reduces this one.
 template <int NV>
-__global__ void __launch_bounds__(1024) norm_q8_kernel(const NormArgs a) {
-  __shared__ float red[32];
+__global__ void __launch_bounds__(NV == 1 ? 256 : 512) norm_q8_kernel(const NormArgs a) {
+  __shared__ __align__(16) float red[2][32];
   const int d = a.d, nv = d >> 3, S = q8_scale_cols(d), nb = (d + kQ8Block - 1) / kQ8Block;
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+  if (threadIdx.x < 64) (&red[0][0])[threadIdx.x] = 0.f;
+  if (blockDim.x < 64 && threadIdx.x + 32 < 64) (&red[0][0])[threadIdx.x + 32] = 0.f;
+  __syncthreads();
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  uint4 x[NV], y[NV];
+  auto load = [&](int t) {
     const int64_t row = static_cast<int64_t>(t) * d;
-    float f[NV][8];
-    float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
-      uint4 v = make_uint4(0, 0, 0, 0), rv = make_uint4(0, 0, 0, 0);
+      x[i] = y[i] = zero;
       if (c < nv) {
-        v = reinterpret_cast<const uint4*>(a.x + row)[c];
-        if (a.residual) rv = reinterpret_cast<const uint4*>(a.residual + row)[c];
+        x[i] = reinterpret_cast<const uint4*>(a.x + row)[c];
+        if (a.residual) y[i] = reinterpret_cast<const uint4*>(a.residual + row)[c];
       }
-      unpack8(v, f[i]);
-      if (a.residual) {
-        float g[8];
-        unpack8(rv, g);
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(f[i][2 * j] + g[2 * j], f[i][2 * j + 1] + g[2 * j + 1]);
-        v = make_uint4(w[0], w[1], w[2], w[3]);
-        unpack8(v, f[i]);
-      }
-      if (a.r && c < nv) reinterpret_cast<uint4*>(a.r + row)[c] = v;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(f[i][j], f[i][j], ss);
     }
-    const float rstd = rsqrtf(block_sum(ss, red) / static_cast<float>(d) + a.eps);
+  };
+  int t = blockIdx.x;
+  if (t < a.T) load(t);
+  for (uint32_t turn = 0; t < a.T; turn ^= 1u) {
+    const int64_t row = static_cast<int64_t>(t) * d;
+    uint4 r[NV];
+    float ss[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
-      float w[8];
-      uint4 wv = make_uint4(0, 0, 0, 0);
-      if (c < nv) wv = reinterpret_cast<const uint4*>(a.w)[c];
-      unpack8(wv, w);
+      r[i] = a.residual ? add_bf16x8(x[i], y[i]) : x[i];
+      if (a.r && c < nv) reinterpret_cast<uint4*>(a.r + row)[c] = r[i];
+      float f[8];
+      unpack8(r[i], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss[0] = fmaf(f[j], f[j], ss[0]);
+    }
+    const int t_row = t;
+    t += gridDim.x;
+    if (t < a.T) load(t);
+    block_sums<1>(ss, red[turn]);
+    const float rstd = rsqrtf(ss[0] / static_cast<float>(d) + a.eps);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+      float f[8], w[8];
+      unpack8(r[i], f);
+      unpack8(c < nv ? __ldg(reinterpret_cast<const uint4*>(a.w) + c) : zero, w);
       uint32_t p[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        p[j] = pack_bf16x2(f[i][2 * j] * rstd * w[2 * j], f[i][2 * j + 1] * rstd * w[2 * j + 1]);
-      const uint4 uv = make_uint4(p[0], p[1], p[2], p[3]);
-      if (a.u && c < nv) reinterpret_cast<uint4*>(a.u + row)[c] = uv;
-      if (a.q) {  // threads past the row hold zeros; a block of 128 is one half warp
-        unpack8(uv, f[i]);
-        const uint32_t s = q8_scale_byte(half_warp_max(c < nv ? amax8(f[i]) : 0u));
+      for (int j = 0; j < 4; ++j) p[j] = pack_bf16x2(f[2 * j] * rstd * w[2 * j], f[2 * j + 1] * rstd * w[2 * j + 1]);
+      const uint4 u = make_uint4(p[0], p[1], p[2], p[3]);
+      if (a.u && c < nv) reinterpret_cast<uint4*>(a.u + row)[c] = u;
+      if (a.q) {  // a block of 128 is one half warp; threads past the row hold zeros
+        unpack8(u, f);
+        const uint32_t s = q8_scale_byte(half_warp_max(c < nv ? amax8(f) : 0u));
         if (c < nv) {
-          reinterpret_cast<uint2*>(a.q + row)[c] = encode8(f[i], s);
-          if ((c & 15) == 0) a.scales[static_cast<int64_t>(t) * S + (c >> 4)] = static_cast<uint8_t>(s);
+          reinterpret_cast<uint2*>(a.q + row)[c] = encode8(f, s);
+          if ((c & 15) == 0) a.scales[static_cast<int64_t>(t_row) * S + (c >> 4)] = static_cast<uint8_t>(s);
         }
       }
     }
     if (a.q && static_cast<int>(threadIdx.x) < S - nb)
-      a.scales[static_cast<int64_t>(t) * S + nb + threadIdx.x] = kQ8PadScale;
+      a.scales[static_cast<int64_t>(t_row) * S + nb + threadIdx.x] = kQ8PadScale;
   }
 }
 
-// dx and this block's share of dw: rows blockIdx.x, blockIdx.x + gridDim.x, ... in order; the
-// row's two sums (of r^2 and of w dy r) are reduced together.
-template <int NV>
+// 16 bytes from global to shared memory, asynchronously; groups are waited for in order.
+__device__ __forceinline__ void copy16_async(uint4* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int n>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+}
+
+// The part of the backward pass that follows a row's two sums: dx of eight columns, and their
+// terms of dw.
+__device__ __forceinline__ void norm_backward_columns(const float (&dy)[8], const float (&r)[8], const float (&w)[8],
+                                                      const uint4& dres, float rstd, float m, float (&dw)[8],
+                                                      bf16* dx) {
+  float e[8];
+  unpack8(dres, e);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    e[j] += rstd * (dy[j] * w[j]) - r[j] * m;
+    dw[j] = fmaf(dy[j], r[j] * rstd, dw[j]);
+  }
+  *reinterpret_cast<uint4*>(dx) = make_uint4(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]),
+                                             pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7]));
+}
+
+__device__ __forceinline__ void store_share(float* part, int64_t at, const float (&dw)[8]) {
+  float4* p = reinterpret_cast<float4*>(part + at);
+  p[0] = make_float4(dw[0], dw[1], dw[2], dw[3]);
+  p[1] = make_float4(dw[4], dw[5], dw[6], dw[7]);
+}
+
+// dx and this block's share of dw, for rows of at most 8192 values: eight columns per
+// thread, rows t, t + grid, ... in order. The rows ahead are copied into a ring of kStages
+// rows in shared memory, so that loads stay in flight through the barrier of the row's sums
+// (of r^2 and of w dy r); each warp reads only what it copied itself.
+constexpr int kBwdStages = 3;
 __global__ void __launch_bounds__(1024) norm_backward_kernel(const NormBwdArgs a) {
-  __shared__ float red[32];
-  const int d = a.d, nv = d >> 3;
-  float w[NV][8], dw[NV][8];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = threadIdx.x + i * blockDim.x;
-    uint4 wv = make_uint4(0, 0, 0, 0);
-    if (c < nv) wv = reinterpret_cast<const uint4*>(a.w)[c];
-    unpack8(wv, w[i]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
-  }
-  const float inv_d = 1.0f / static_cast<float>(d);
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const int64_t row = static_cast<int64_t>(t) * d;
-    float dy[NV][8], r[NV][8];
-    float ss = 0.f, sg = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = threadIdx.x + i * blockDim.x;
-      uint4 rv = make_uint4(0, 0, 0, 0);
-      float4 y0 = make_float4(0.f, 0.f, 0.f, 0.f), y1 = y0;
-      if (c < nv) {
-        rv = reinterpret_cast<const uint4*>(a.r + row)[c];
-        y0 = reinterpret_cast<const float4*>(a.dy + row)[2 * c];
-        y1 = reinterpret_cast<const float4*>(a.dy + row)[2 * c + 1];
-      }
-      unpack8(rv, r[i]);
-      dy[i][0] = y0.x, dy[i][1] = y0.y, dy[i][2] = y0.z, dy[i][3] = y0.w;
-      dy[i][4] = y1.x, dy[i][5] = y1.y, dy[i][6] = y1.z, dy[i][7] = y1.w;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        ss = fmaf(r[i][j], r[i][j], ss);
-        sg = fmaf(dy[i][j] * w[i][j], r[i][j], sg);
-      }
-    }
-    const float rstd = rsqrtf(block_sum(ss, red) * inv_d + a.eps);
-    const float k = block_sum(sg, red) * inv_d * rstd * rstd * rstd;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = threadIdx.x + i * blockDim.x;
-      if (c < nv) {
-        float e[8];
-        uint4 ev = make_uint4(0, 0, 0, 0);
-        if (a.dres) ev = reinterpret_cast<const uint4*>(a.dres + row)[c];
-        unpack8(ev, e);
-        uint32_t p[4];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          e[j] += rstd * (dy[i][j] * w[i][j]) - r[i][j] * k;
-          dw[i][j] = fmaf(dy[i][j], r[i][j] * rstd, dw[i][j]);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) p[j] = pack_bf16x2(e[2 * j], e[2 * j + 1]);
-        reinterpret_cast<uint4*>(a.dx + row)[c] = make_uint4(p[0], p[1], p[2], p[3]);
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = threadIdx.x + i * blockDim.x;
-    if (c < nv) {
-      float4* p = reinterpret_cast<float4*>(a.part + static_cast<int64_t>(blockIdx.x) * d) + 2 * c;
-      p[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
-      p[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
-    }
-  }
-}
-
-// dw[c] = the blocks' shares added in a fixed order: 32 row groups of consecutive blocks,
-// then the groups in order.
-__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__ part, int G, int d,
-                                                       float* __restrict__ dw) {
-  __shared__ float s[32][33];
-  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-  const int per = (G + 31) / 32, b0 = g * per, b1 = min(G, b0 + per);
-  float v = 0.f;
-  if (c < d)
-    for (int b = b0; b < b1; ++b) v += part[static_cast<int64_t>(b) * d + c];
-  s[g][lane] = v;
+  extern __shared__ __align__(16) uint4 ring[];
+  __shared__ __align__(16) float red[2][64];
+  const int d = a.d, nv = d >> 3, lane = threadIdx.x & 31, c = threadIdx.x, B = blockDim.x;
+  for (int i = threadIdx.x; i < 128; i += B) (&red[0][0])[i] = 0.f;
   __syncthreads();
-  if (g == 0 && c < d) {
-    float t = 0.f;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const bool on = c < nv;
+  // dy leaves in the order of its lines: 64 units of 16 bytes per warp, two of them a lane's
+  const int u0 = 2 * (c - lane) + lane;
+  auto load = [&](int t, int stage) {
+    if (t < a.T) {
+      uint4* s = ring + static_cast<int64_t>(stage) * 4 * B;
+      const int64_t row = static_cast<int64_t>(t) * d;
+      const uint4* y = reinterpret_cast<const uint4*>(a.dy + row);
+      if (u0 < 2 * nv) copy16_async(s + u0, y + u0);
+      if (u0 + 32 < 2 * nv) copy16_async(s + u0 + 32, y + u0 + 32);
+      if (on) {
+        copy16_async(s + 2 * B + c, reinterpret_cast<const uint4*>(a.r + row) + c);
+        if (a.dres) copy16_async(s + 3 * B + c, reinterpret_cast<const uint4*>(a.dres + row) + c);
+      }
+    }
+    copy_commit();
+  };
+  float w[8], dw[8] = {};
+  unpack8(on ? reinterpret_cast<const uint4*>(a.w)[c] : zero, w);
+  const float inv_d = 1.0f / static_cast<float>(d);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) t += s[i][lane];
-    dw[c] = t;
+  for (int i = 0; i < kBwdStages - 1; ++i) load(blockIdx.x + i * gridDim.x, i);
+  int stage = 0;
+  uint32_t turn = 0;
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1u) {
+    // into the row before this one, which every warp has read before the last barrier
+    load(t + (kBwdStages - 1) * gridDim.x, stage == 0 ? kBwdStages - 1 : stage - 1);
+    copy_wait<kBwdStages - 1>();
+    __syncwarp();
+    const uint4* s = ring + static_cast<int64_t>(stage) * 4 * B;
+    float dy[8] = {}, r[8] = {};
+    uint4 dres = zero;
+    if (on) {
+      const float4 y0 = reinterpret_cast<const float4*>(s)[2 * c], y1 = reinterpret_cast<const float4*>(s)[2 * c + 1];
+      dy[0] = y0.x, dy[1] = y0.y, dy[2] = y0.z, dy[3] = y0.w;
+      dy[4] = y1.x, dy[5] = y1.y, dy[6] = y1.z, dy[7] = y1.w;
+      unpack8(s[2 * B + c], r);
+      if (a.dres) dres = s[3 * B + c];
+    }
+    float sums[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      sums[0] = fmaf(r[j], r[j], sums[0]);
+      sums[1] = fmaf(dy[j] * w[j], r[j], sums[1]);
+    }
+    block_sums<2>(sums, red[turn]);
+    const float rstd = rsqrtf(sums[0] * inv_d + a.eps);
+    if (on)
+      norm_backward_columns(dy, r, w, dres, rstd, sums[1] * inv_d * rstd * rstd * rstd, dw,
+                            a.dx + static_cast<int64_t>(t) * d + 8 * c);
+    stage = stage + 1 == kBwdStages ? 0 : stage + 1;
+  }
+  if (on) store_share(a.part, static_cast<int64_t>(blockIdx.x) * d + 8 * c, dw);
+}
+
+// The same for longer rows, which a ring in shared memory would not hold: 8 NV columns per
+// thread, loaded into registers.
+template <int NV>
+__global__ void __launch_bounds__(512) norm_backward_long_kernel(const NormBwdArgs a) {
+  __shared__ __align__(16) float red[2][64];
+  const int d = a.d, nv = d >> 3;
+  for (int i = threadIdx.x; i < 128; i += blockDim.x) (&red[0][0])[i] = 0.f;
+  __syncthreads();
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  float dw[NV][8] = {};
+  const float inv_d = 1.0f / static_cast<float>(d);
+  uint32_t turn = 0;
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1u) {
+    const int64_t row = static_cast<int64_t>(t) * d;
+    float sums[2] = {0.f, 0.f};
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {  // the second pass reads the row again, from L2
+      const float rstd = rsqrtf(sums[0] * inv_d + a.eps), m = sums[1] * inv_d * rstd * rstd * rstd;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        if (c >= nv) continue;
+        float r[8], w[8];
+        unpack8(reinterpret_cast<const uint4*>(a.r + row)[c], r);
+        unpack8(__ldg(reinterpret_cast<const uint4*>(a.w) + c), w);
+        const float4 y0 = reinterpret_cast<const float4*>(a.dy + row)[2 * c];
+        const float4 y1 = reinterpret_cast<const float4*>(a.dy + row)[2 * c + 1];
+        const float dy[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+        if (pass == 0) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            sums[0] = fmaf(r[j], r[j], sums[0]);
+            sums[1] = fmaf(dy[j] * w[j], r[j], sums[1]);
+          }
+        } else {
+          norm_backward_columns(dy, r, w, a.dres ? reinterpret_cast<const uint4*>(a.dres + row)[c] : zero, rstd, m,
+                                dw[i], a.dx + row + 8 * c);
+        }
+      }
+      if (pass == 0) block_sums<2>(sums, red[turn]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = threadIdx.x + i * blockDim.x;
+    if (c < nv) store_share(a.part, static_cast<int64_t>(blockIdx.x) * d + 8 * c, dw[i]);
   }
 }
 
-// Vectors of eight per thread and threads of a block that holds one row of d values.
-int norm_vectors(int d) { return d <= 8192 ? 1 : d <= 16384 ? 2 : 4; }
+// dw of eight columns per block: the blocks' shares are added in a fixed order, 128 groups of
+// rows (two threads of four columns each) and then the groups. (32 columns per block keeps
+// too few SMs busy.)
+__global__ void __launch_bounds__(256) norm_dw_kernel(const float* __restrict__ part, int G, int d,
+                                                      float* __restrict__ dw) {
+  __shared__ float s[128][9];
+  const int g = threadIdx.x >> 1, c = (threadIdx.x & 1) * 4, col = blockIdx.x * 8 + c;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int b = g; b < G; b += 128) {
+    const float4 p = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(b) * d + col);
+    v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
+  }
+  s[g][c] = v.x, s[g][c + 1] = v.y, s[g][c + 2] = v.z, s[g][c + 3] = v.w;
+  __syncthreads();
+  // warp w sums column w: four groups per lane, then a butterfly
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  float t = (s[lane][w] + s[lane + 32][w]) + (s[lane + 64][w] + s[lane + 96][w]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  if (lane == 0) dw[blockIdx.x * 8 + w] = t;
+}
+
+// How a block holds rows of d values: vectors of eight per thread, threads.
+int norm_vectors(int d) { return d <= 2048 ? 1 : d <= 8192 ? 2 : d <= 16384 ? 4 : 8; }
 int norm_threads(int d) {
   const int per = norm_vectors(d) * 8;
-  return (((d + per - 1) / per) + 31) / 32 * 32;
+  return ((d + per - 1) / per + 31) / 32 * 32;
 }
 
 }  // namespace
@@ -308,7 +419,7 @@ cudaError_t launch_quantize_rows(const bf16* x, int64_t R, int C, uint8_t* q, ui
 cudaError_t launch_quantize_weights(const bf16* W, int E, int N, int K, uint8_t* q, uint8_t* scales, int num_sms,
                                     cudaStream_t s) {
   const int64_t tiles = static_cast<int64_t>(E) * ((N + kQ8Block - 1) / kQ8Block) * ((K + kQ8Block - 1) / kQ8Block);
-  int64_t grid = 8 * num_sms;
+  int64_t grid = 4 * num_sms;
   if (grid > tiles) grid = tiles;
   if (grid < 1) return cudaSuccess;
   quantize_weights_kernel<<<static_cast<int>(grid), 256, 0, s>>>(W, tiles, N, K, q, scales);
@@ -316,31 +427,49 @@ cudaError_t launch_quantize_weights(const bf16* W, int E, int N, int K, uint8_t*
 }
 
 cudaError_t launch_norm_q8(const NormArgs& a, int num_sms, cudaStream_t s) {
-  const int threads = norm_threads(a.d), nv = norm_vectors(a.d);
-  const int grid = a.T;
-  (void)num_sms;
+  const int nv = norm_vectors(a.d), threads = norm_threads(a.d);
+  const int64_t resident = static_cast<int64_t>(num_sms) * (1024 / threads);
+  const int grid = static_cast<int>(a.T < resident ? a.T : resident);
   if (nv == 1) norm_q8_kernel<1><<<grid, threads, 0, s>>>(a);
   else if (nv == 2) norm_q8_kernel<2><<<grid, threads, 0, s>>>(a);
-  else norm_q8_kernel<4><<<grid, threads, 0, s>>>(a);
+  else if (nv == 4) norm_q8_kernel<4><<<grid, threads, 0, s>>>(a);
+  else norm_q8_kernel<8><<<grid, threads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
+namespace {
+constexpr int kBwdRingMax = 8192;  // longest row of norm_backward_kernel
+int bwd_threads(int d) { return d <= kBwdRingMax ? (d / 8 + 31) / 32 * 32 : 512; }
+int bwd_ring_bytes(int d) { return d <= kBwdRingMax ? kBwdStages * bwd_threads(d) * 64 : 0; }
+}  // namespace
+
+// Blocks of the backward pass: as many as are resident at once (1024 threads and about 200 KB
+// of rings per SM).
 int norm_backward_blocks(int64_t T, int d, int num_sms) {
-  const int threads = norm_threads(d);
-  const int per_sm = threads >= 1024 ? 1 : 1024 / threads;
-  const int64_t g = static_cast<int64_t>(num_sms < kNormMaxSms ? num_sms : kNormMaxSms) * per_sm;
-  return static_cast<int>(g < T ? g : T);
+  int per_sm = 1024 / bwd_threads(d);
+  if (d <= kBwdRingMax) per_sm = std::min(per_sm, 204800 / bwd_ring_bytes(d));
+  const int64_t g = static_cast<int64_t>(std::min(num_sms, kNormMaxSms)) * std::max(per_sm, 1);
+  return static_cast<int>(std::min(g, T));
 }
 
 cudaError_t launch_norm_backward(const NormBwdArgs& a, float* dw, int num_sms, cudaStream_t s) {
-  const int threads = norm_threads(a.d), nv = norm_vectors(a.d);
+  const int threads = bwd_threads(a.d), ring = bwd_ring_bytes(a.d);
   const int grid = norm_backward_blocks(a.T, a.d, num_sms);
-  if (nv == 1) norm_backward_kernel<1><<<grid, threads, 0, s>>>(a);
-  else if (nv == 2) norm_backward_kernel<2><<<grid, threads, 0, s>>>(a);
-  else norm_backward_kernel<4><<<grid, threads, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = cudaSuccess;
+  if (a.d <= kBwdRingMax) {
+    if (ring > 48 * 1024)
+      e = cudaFuncSetAttribute(norm_backward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kBwdStages * 1024 * 64);
+    if (e != cudaSuccess) return e;
+    norm_backward_kernel<<<grid, threads, ring, s>>>(a);
+  } else if (a.d <= 16384) {
+    norm_backward_long_kernel<4><<<grid, threads, 0, s>>>(a);
+  } else {
+    norm_backward_long_kernel<8><<<grid, threads, 0, s>>>(a);
+  }
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  norm_dw_kernel<<<(a.d + 31) / 32, 1024, 0, s>>>(a.part, grid, a.d, dw);
+  norm_dw_kernel<<<a.d / 8, 256, 0, s>>>(a.part, grid, a.d, dw);
   return cudaGetLastError();
 }
 
