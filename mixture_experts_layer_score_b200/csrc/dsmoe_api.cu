@@ -115,6 +115,20 @@ bool map_bytes(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t rows, u
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The weights [outer, rows, inner] of a plain 8-bit product with even and odd rows apart: 4D
+// (inner, 2, rows / 2, outer), box (128, 1, 128, 1). rows is even.
+bool map_bytes_pairs(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t rows, uint64_t outer) {
+  auto enc = tensor_map_encoder();
+  if (!enc || rows % 2) return false;
+  cuuint64_t dims[4] = {inner, 2, rows / 2, outer};
+  cuuint64_t strides[3] = {inner, 2 * inner, inner * rows};
+  cuuint32_t box[4] = {128, 1, 128, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 4D bf16 view (64, rows, cols / 64, experts) of an [experts, rows, cols] tensor whose
 // cols are contiguous, 128-byte swizzle, box (64, 64, 4, 1): one copy lands 256 cols x 64
 // rows as four MN-major atoms (the backward GEMMs' A operand).
@@ -1878,8 +1892,8 @@ dsmoe_status q8_matmul(dsmoe_handle* h, int32_t E, int64_t R, int32_t N, int32_t
   dsmoe::Q8GemmArgs g;
   memset(&g, 0, sizeof(g));
   const int tok = dsmoe::q8_token_tile(R, E, K);
-  if (!map_bytes(&g.map_a, a, K, R, 1, dsmoe::q8_box_rows(tok)) || !map_bytes(&g.map_w0, W, K, N, E, 128, true) ||
-      !map_bytes(&g.map_w1, W1 ? W1 : W, K, N, E, 128, true))
+  if (!map_bytes(&g.map_a, a, K, R, 1, dsmoe::q8_box_rows(tok)) || !(W1 ? map_bytes(&g.map_w0, W, K, N, E, 128, true) && map_bytes(&g.map_w1, W1, K, N, E, 128, true)
+           : map_bytes_pairs(&g.map_w0, W, K, N, E)))
     return fail(DSMOE_ERR_CUDA, "cuTensorMapEncodeTiled rejected a tensor map of this call");
   g.a_scales = static_cast<const uint8_t*>(a_scales);
   g.W_scales = static_cast<const uint8_t*>(W_scales);

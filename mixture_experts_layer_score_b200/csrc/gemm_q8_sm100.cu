@@ -11,7 +11,8 @@
 //
 // Orientation as in the bf16 grouped GEMM (gemm_sm100.cu): M = 128 output features per chain,
 // N = the tile's tokens rounded up to 16, two chains sharing the token operand (gated: the
-// same 128 features of W_gate and W_up; plain: 256 consecutive features).
+// same 128 features of W_gate and W_up; plain: the even and the odd ones of 256 features, so
+// that a thread's two accumulators are neighbours in the output row).
 //
 // One CTA per SM, 352 threads:
 //   warp 0      TMA producer: per 128-wide K block two 128 x 128 weight tiles and a
@@ -109,6 +110,15 @@ __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t saddr)
   d |= static_cast<uint64_t>(128 >> 4) << 32;  // stride byte offset: next eight rows
   d |= static_cast<uint64_t>(1) << 46;         // descriptor version for sm_100
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t c0, int32_t c1,
+                                            int32_t c2, int32_t c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+      "[%2];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
 }
 
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -272,9 +282,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
           }
           mbar_arrive_expect_tx(&full[stage], stage_bytes);
           uint8_t* w = sW + stage * kWBytes;
-          tma_load_3d(w, &a.map_w0, &full[stage], kb * kBK, n0, t.expert);
-          tma_load_3d(w + kWBytes / 2, kGated ? &a.map_w1 : &a.map_w0, &full[stage], kb * kBK,
-                      kGated ? n0 : n0 + kFeat, t.expert);
+          if (kGated) {  // the same 128 rows of W_gate and W_up
+            tma_load_3d(w, &a.map_w0, &full[stage], kb * kBK, n0, t.expert);
+            tma_load_3d(w + kWBytes / 2, &a.map_w1, &full[stage], kb * kBK, n0, t.expert);
+          } else {  // the even and the odd rows of 256
+            tma_load_4d(w, &a.map_w0, &full[stage], kb * kBK, 0, n0 >> 1, t.expert);
+            tma_load_4d(w + kWBytes / 2, &a.map_w0, &full[stage], kb * kBK, 1, n0 >> 1, t.expert);
+          }
           for (int i = 0; i < boxes; ++i)
             tma_load_2d(sX + stage * G_::kXBytes + i * G_::kBoxRows * kBK, &a.map_a, &full[stage], kb * kBK,
                         t.row0 + i * static_cast<int>(G_::kBoxRows));
@@ -329,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
           const uint32_t s0 = smem_addr(sSf + slot * G_::kSfBytes);
           if (elect_one()) {
             tmem_copy_scales(sf, s0);
-            tmem_copy_scales(sf + 4, s0 + 512);
+            if (kGated) tmem_copy_scales(sf + 4, s0 + 512);
             tmem_copy_scales(sf + 8, s0 + 1024);
             if (n_mma > 128) tmem_copy_scales(sf + 12, s0 + 1536);
           }
@@ -350,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
             const uint64_t dk = static_cast<uint64_t>(2 * k);
             const uint32_t accum = (kb | k) ? 1u : 0u;
             mma_q8_ss(d0, w0 + dk, xd + dk, di, sf, sf + 8, accum);
-            mma_q8_ss(d0 + kTok, w1 + dk, xd + dk, di, sf + 4, sf + 8, accum);
+            mma_q8_ss(d0 + kTok, w1 + dk, xd + dk, di, kGated ? sf + 4 : sf, sf + 8, accum);
           }
           mma_commit(&empty[stage]);
           if (id == 3 || kb == kb_n - 1) mma_commit(&sf_empty[quad % kSfSlots]);
@@ -402,8 +416,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
           break;
         }
         uint4* dst = reinterpret_cast<uint4*>(sSf + slot * G_::kSfBytes) + lane;
-        dst[0] = make_uint4(g0, g0, g0, g0);
-        dst[32] = make_uint4(g1, g1, g1, g1);
+        if (kGated) {
+          dst[0] = make_uint4(g0, g0, g0, g0);
+          dst[32] = make_uint4(g1, g1, g1, g1);
+        } else {  // both chains: rows 0-63 are of the first block of 128 features, 64-127 of the second
+          dst[0] = make_uint4(g0, g0, g1, g1);
+        }
         dst[64] = make_uint4(w[0], w[1], w[2], w[3]);
         if (kTok > 128) dst[96] = make_uint4(w[4], w[5], w[6], w[7]);
         fence_proxy_async();
@@ -447,27 +465,28 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
       // rounded into one register), so that the next tile's MMAs may overwrite them ...
       uint32_t hold[kHold][kChunk], hold1[kOut == kOutF32 ? kHold : 1][kChunk];
       uint32_t v0[2][kChunk], v1[2][kChunk];
-      if (half < n_chunks) {
-        tmem_ld8(tb + kChunk * half, v0[0]);
-        tmem_ld8(tb + kTok + kChunk * half, v1[0]);
-      }
 #pragma unroll
-      for (int i = 0; i < kHold; ++i) {
-        const int c = 2 * i + half;
-        if (c >= n_chunks) break;
-        tmem_wait_ld();
-        if (i + 1 < kHold && c + 2 < n_chunks) {
-          tmem_ld8(tb + kChunk * (c + 2), v0[(i + 1) & 1]);
-          tmem_ld8(tb + kTok + kChunk * (c + 2), v1[(i + 1) & 1]);
+      for (int i = 0; i < kHold; i += 2) {  // two chunks at a time
+        if (2 * i + half >= n_chunks) break;
+        const uint32_t at = tb + kChunk * (2 * i + half);
+        tmem_ld8(at, v0[0]);
+        tmem_ld8(at + kTok, v1[0]);
+        if (i + 1 < kHold) {  // (columns past the tile's tokens hold what nothing reads)
+          tmem_ld8(at + 2 * kChunk, v0[1]);
+          tmem_ld8(at + 2 * kChunk + kTok, v1[1]);
         }
+        tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) {
-          const float x = __uint_as_float(v0[i & 1][j]), y = __uint_as_float(v1[i & 1][j]);
-          if (kGated) hold[i][j] = __float_as_uint(__fdividef(x, 1.0f + __expf(-x)) * y);
-          else if (kOut == kOutBf16) hold[i][j] = pack_bf16x2(x, y);
+        for (int j = 0; j < 2 * kChunk; ++j) {
+          const int s = j >= kChunk ? 1 : 0;
+          if (i + s >= kHold) break;
+          const uint32_t u = v0[s][j & 7], v = v1[s][j & 7];
+          const float x = __uint_as_float(u), y = __uint_as_float(v);
+          if (kGated) hold[i + s][j & 7] = __float_as_uint(__fdividef(x, 1.0f + __expf(-x)) * y);
+          else if (kOut == kOutBf16) hold[i + s][j & 7] = pack_bf16x2(x, y);
           else {
-            hold[i][j] = v0[i & 1][j];
-            hold1[kOut == kOutF32 ? i : 0][j] = v1[i & 1][j];
+            hold[i + s][j & 7] = u;
+            hold1[kOut == kOutF32 ? i + s : 0][j & 7] = v;
           }
         }
       }
@@ -480,23 +499,17 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
 #pragma unroll
       for (int i = 0; i < kHold; i += 2) {
         if (2 * i + half >= n_chunks) break;
-        float* st = reinterpret_cast<float*>(stg + buf * kStgBytes);
-        float* st1 = reinterpret_cast<float*>(stg + (buf ^ 1u) * kStgBytes);
-        uint16_t* sh = reinterpret_cast<uint16_t*>(st);
-        if (kOut == kOutF32) group_sync(half);  // both buffers are free
+        uint32_t* st = reinterpret_cast<uint32_t*>(stg + (kOut == kOutF32 ? 0 : buf * kStgBytes));
+        if (kOut == kOutF32) group_sync(half);  // both buffers are one, and free
 #pragma unroll
         for (int j = 0; j < 2 * kChunk; ++j) {
           const int ii = i + (j >= kChunk ? 1 : 0);
           if (ii >= kHold) break;
-          const uint32_t v = hold[ii][j & (kChunk - 1)];
-          if (kGated) st[j * kFeat + q * 32 + lane] = __uint_as_float(v);
-          else if (kOut == kOutBf16) {
-            sh[j * 2 * kFeat + q * 32 + lane] = static_cast<uint16_t>(v);
-            sh[j * 2 * kFeat + kFeat + q * 32 + lane] = static_cast<uint16_t>(v >> 16);
-          } else {
-            st[j * kFeat + q * 32 + lane] = __uint_as_float(v);
-            st1[j * kFeat + q * 32 + lane] = __uint_as_float(hold1[kOut == kOutF32 ? ii : 0][j & (kChunk - 1)]);
-          }
+          const uint32_t v = hold[ii][j & 7];  // gated: feature 32 q + lane; else two features
+          if (kOut != kOutF32) st[j * kFeat + q * 32 + lane] = v;
+          else
+            reinterpret_cast<uint2*>(st)[j * kFeat + q * 32 + lane] =
+                make_uint2(v, hold1[kOut == kOutF32 ? ii : 0][j & 7]);
         }
         group_sync(half);
 #pragma unroll
@@ -518,13 +531,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
             if (lane == 0) a.q_scales[row * So + t.n_blk] = static_cast<uint8_t>(s);
             if (t.n_blk == nbo - 1 && lane < So - nbo) a.q_scales[row * So + nbo + lane] = kQ8PadScale;
           } else if (kOut == kOutBf16) {
-            const uint4 o = reinterpret_cast<const uint4*>(sh)[j * (2 * kFeat / 8) + lane];
+            const uint4 o = reinterpret_cast<const uint4*>(st)[j * (2 * kFeat / 8) + lane];
             const int f = n0 + 8 * lane;
             if (f < a.N) *reinterpret_cast<uint4*>(a.out + row * a.N + f) = o;
           } else {
 #pragma unroll
             for (int ch = 0; ch < 2; ++ch) {
-              float4 o = reinterpret_cast<const float4*>(ch ? st1 : st)[j * (kFeat / 4) + lane];
+              float4 o = reinterpret_cast<const float4*>(st)[j * (2 * kFeat / 4) + ch * 32 + lane];
               const int f = n0 + ch * kFeat + 4 * lane;
               if (f < a.N) {
                 const int64_t at = row * a.N + f;

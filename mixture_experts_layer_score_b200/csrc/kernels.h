@@ -342,8 +342,9 @@ cudaError_t launch_norm_backward(const NormBwdArgs& a, float* dw, int num_sms, c
 // it, to what out_f32 holds.
 struct Q8GemmArgs {
   CUtensorMap map_a;         // 2D [R, K] bytes, box (128, q8_box_rows(token tile))
-  CUtensorMap map_w0;        // 3D (K, N, experts) bytes, box (128, 128): W (gated: W_gate)
-  CUtensorMap map_w1;        // gated: W_up
+  CUtensorMap map_w0;        // bytes: gated, W_gate as 3D (K, N, experts), box (128, 128, 1); plain, W
+                             // as 4D (K, 2, N / 2, experts), box (128, 1, 128, 1)
+  CUtensorMap map_w1;        // gated: W_up, as W_gate
   const uint8_t* a_scales;   // [R, q8_scale_cols(K)]
   const uint8_t* W_scales;   // [E, ceil(N / 128), q8_scale_cols(K)]
   const uint8_t* W1_scales;
