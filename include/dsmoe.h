@@ -604,7 +604,7 @@ dsmoe_status dsmoe_norm_backward(dsmoe_handle* h, int32_t T, const float* dy, co
 /*
  * Grouped products of 8-bit rows with 8-bit expert weights: rows offsets[e] .. offsets[e+1]
  * of a [R, K] use expert e's weights (offsets int32 [E + 1] on the device, not decreasing,
- * within [0, R]; E = 1 with {0, R} is a plain product). Output rows outside
+ * within [0, R]; NULL with E = 1 is a plain product of all rows). Output rows outside
  * [offsets[0], offsets[E]) are left as they were. Products of e4m3 values and scales are
  * summed in fp32. Offsets outside [0, R] are clipped to it and a group that would end
  * before it starts is empty, so that nothing outside the tensors is touched; what
@@ -622,6 +622,33 @@ dsmoe_status dsmoe_q8_gated_matmul(dsmoe_handle* h, int32_t E, int64_t R, int32_
                                    const int32_t* offsets, const void* a, const void* a_scales, const void* W_gate,
                                    const void* gate_scales, const void* W_up, const void* up_scales, void* q,
                                    void* scales, void* stream);
+
+/*
+ * The layer forward on 8-bit rows and 8-bit expert weights: dsmoe_forward's routing (the
+ * bf16 rows x and W_router decide it, so it is the bf16 layer's), the experts' two products
+ * as dsmoe_q8_gated_matmul and dsmoe_q8_matmul, and the combine
+ *   h_t = base_t + sum_shared FFN(u_t) + sum_k g_{t,k} FFN_{e(t,k)}(u_t)
+ * with base = residual where it is given (a block in front of whose layer stands
+ * dsmoe_norm_q8: x its u, residual its r), else x.
+ *   x         bf16 [T, d]; x_q, x_scales its 8-bit rows (dsmoe_norm_q8, dsmoe_q8_quantize)
+ *   residual  bf16 [T, d] or NULL
+ *   weights   device pointers of dsmoe_q8_quantize_weights' outputs, values and scales:
+ *             W_gate, W_up [N', F, d], W_down [N', d, F] (the handle's expert range only),
+ *             Ws_gate, Ws_up [K_s, F_s, d], Ws_down [K_s, d, F_s] (NULL where the handle
+ *             adds no shared experts)
+ * The other arguments, outputs, errors, expert ranges (dsmoe_set_expert_range), selection
+ * variants and timing are dsmoe_forward's. Of the workspace, "Xp", "A1" and "A1s" hold 8-bit
+ * rows afterwards, and a training forward or dsmoe_ep_route before it is forgotten
+ * (dsmoe_backward_experts, dsmoe_backward_weights and dsmoe_ep_combine then refuse).
+ */
+typedef struct dsmoe_q8_weights {
+  const void *W_gate, *W_gate_scales, *W_up, *W_up_scales, *W_down, *W_down_scales;
+  const void *Ws_gate, *Ws_gate_scales, *Ws_up, *Ws_up_scales, *Ws_down, *Ws_down_scales;
+} dsmoe_q8_weights;
+dsmoe_status dsmoe_forward_q8(dsmoe_handle* h, int32_t T, const void* x, const void* x_q, const void* x_scales,
+                              const void* residual, const int32_t* token_ids, const void* W_router, const float* b,
+                              const dsmoe_q8_weights* weights, void* h_out, int32_t* topk_idx, float* gates,
+                              int32_t* counts, float* f, float* P, float* P_sum, float* scores_dbg, void* stream);
 
 #ifdef __cplusplus
 }  /* extern "C" */

@@ -5,7 +5,7 @@ declared in include/dsmoe.h); this package is its ctypes binding plus the
 multi-GPU token-sharding helper.
 """
 from .binding import *  # noqa: F401,F403
-from .binding import (DSMoE, DsmoeCfg, DsmoeError, make_cfg, cfg_from, dsmoe_create, dsmoe_destroy,
+from .binding import (DSMoE, DSMoEQ8, DsmoeCfg, DsmoeQ8Weights, DsmoeError, make_cfg, cfg_from, dsmoe_create, dsmoe_destroy,
                       dsmoe_forward, dsmoe_forward_host, dsmoe_balance_stats, dsmoe_get_status,
                       dsmoe_set_wait_limit, dsmoe_set_timing, dsmoe_stage_times, dsmoe_stage_name,
                       dsmoe_launch_count, dsmoe_check_config, dsmoe_workspace_bytes, dsmoe_abi_version,

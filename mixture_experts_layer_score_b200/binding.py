@@ -36,7 +36,7 @@ ABI_FUNCTIONS = (
     "dsmoe_ep_combine", "dsmoe_forward_host_async", "dsmoe_host_join", "dsmoe_host_sync", "dsmoe_set_training",
     "dsmoe_backward_experts", "dsmoe_backward_weights", "dsmoe_gemm_role_cycles",
     "dsmoe_q8_scale_cols", "dsmoe_q8_quantize", "dsmoe_q8_quantize_weights", "dsmoe_norm_q8", "dsmoe_norm_backward",
-    "dsmoe_q8_matmul", "dsmoe_q8_gated_matmul",
+    "dsmoe_q8_matmul", "dsmoe_q8_gated_matmul", "dsmoe_forward_q8",
 )
 ROLE_CTAS, ROLE_SLOTS = 160, 9
 ROLE_KINDS = ("gemm_down", "gemm_gate_up", "shared_down", "shared_gate_up", "weight_grad")
@@ -49,6 +49,13 @@ class DsmoeCfg(ctypes.Structure):
                 ("d_ff", ctypes.c_int32), ("n_shared", ctypes.c_int32), ("d_ff_shared", ctypes.c_int32),
                 ("score", ctypes.c_int32), ("bias_mode", ctypes.c_int32), ("renormalize", ctypes.c_int32),
                 ("max_tokens", ctypes.c_int32), ("hash_mult", ctypes.c_uint32), ("hash_mod", ctypes.c_uint32)]
+
+
+Q8_WEIGHTS = ("W_gate", "W_up", "W_down", "Ws_gate", "Ws_up", "Ws_down")
+
+
+class DsmoeQ8Weights(ctypes.Structure):
+    _fields_ = [(n + s, ctypes.c_void_p) for n in Q8_WEIGHTS for s in ("", "_scales")]
 
 
 class DsmoeError(RuntimeError):
@@ -111,6 +118,7 @@ def _load():
         "dsmoe_backward_router": (ctypes.c_int, [vp, i32, vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp,
                                                  vp]),
         "dsmoe_q8_scale_cols": (i32, [i32]),
+        "dsmoe_forward_q8": (ctypes.c_int, [vp, i32] + [vp] * 7 + [ctypes.POINTER(DsmoeQ8Weights)] + [vp] * 8 + [vp]),
         "dsmoe_q8_quantize": (ctypes.c_int, [vp, i64, i32] + [vp] * 3 + [vp]),
         "dsmoe_q8_quantize_weights": (ctypes.c_int, [vp, i32, i32, i32] + [vp] * 3 + [vp]),
         "dsmoe_norm_q8": (ctypes.c_int, [vp, i32, vp, vp, vp, ctypes.c_float] + [vp] * 4 + [vp]),
@@ -510,6 +518,24 @@ def dsmoe_q8_gated_matmul(handle, E, R, N, K, offsets, a, a_scales, W_gate, gate
     _check(_lib.dsmoe_q8_gated_matmul(handle, E, R, N, K, *p, s), where)
 
 
+def dsmoe_forward_q8(handle, T, x, x_q, x_scales, residual, token_ids, W_router, b, weights, h, topk_idx, gates,
+                     counts, f, P, P_sum=None, scores_dbg=None, stream=None) -> None:
+    """weights: a DsmoeQ8Weights, or a dict of (values, scales) tensor pairs by name (Q8_WEIGHTS)."""
+    where, T = "dsmoe_forward_q8", int(T)
+    if not isinstance(weights, DsmoeQ8Weights):
+        pairs = {n: weights.get(n) or (None, None) for n in Q8_WEIGHTS}
+        weights = DsmoeQ8Weights(*[_ptr(t) for n in Q8_WEIGHTS for t in pairs[n]])
+    d = _handles[handle][1] if handle in _handles else 0
+    n = T * d
+    rows = (("x", x, "bf16", n), ("x_q", x_q, "q8", n), ("x_scales", x_scales, "q8", T * dsmoe_q8_scale_cols(d)),
+            ("residual", residual, "bf16", n))
+    (x, x_q, x_scales, residual), s = _take(where, handle, stream, *rows)
+    st = _lib.dsmoe_forward_q8(handle, T, x, x_q, x_scales, residual, _ptr(token_ids), _ptr(W_router), _ptr(b),
+                               ctypes.byref(weights), *[_ptr(t) for t in (
+                                   h, topk_idx, gates, counts, f, P, P_sum, scores_dbg)], s)
+    _check(st, where)
+
+
 _WS_DTYPES = {"logits": "float32", "offsets": "int32", "slot_of": "int32", "Xp": "bfloat16",
               "A1": "bfloat16", "A1s": "bfloat16", "Y": "bfloat16", "Hs": "float32", "AB": "bfloat16",
               "ABs": "bfloat16", "dAB": "bfloat16", "dABs": "bfloat16", "dXp": "bfloat16", "dXs": "float32"}
@@ -605,4 +631,61 @@ class DSMoE:
         dsmoe_forward(self.handle, T, x, token_ids, w.get("W_router"), w.get("b"), w["W_gate"], w["W_up"],
                       w["W_down"], w.get("Ws_gate"), w.get("Ws_up"), w.get("Ws_down"), o["h"], o["topk_idx"],
                       o["gates"], o["counts"], o["f"], o["P"], o["P_sum"], o["scores"], stream)
+        return o
+
+
+class DSMoEQ8(DSMoE):
+    """The layer with its expert weights in 8 bits. weights: DSMoE's dict; the six expert tensors
+    may be bf16 (quantised here, once; the bf16 tensors are not kept) or (values, scales)
+    pairs that already are in 8 bits."""
+
+    def __init__(self, cfg: DsmoeCfg, weights: Dict, device: int = 0):
+        import torch
+        super().__init__(cfg, {k: v for k, v in weights.items() if k not in Q8_WEIGHTS}, device)
+        self.q = {}
+        for name in Q8_WEIGHTS:
+            W = weights.get(name)
+            if W is not None and not isinstance(W, (tuple, list)):
+                E, N, K = W.shape
+                if E == 0:
+                    continue
+                values = torch.empty((E, N, K), dtype=torch.float8_e4m3fn, device=W.device)
+                scales = torch.empty((E, -(-N // 128), dsmoe_q8_scale_cols(K)), dtype=torch.float8_e8m0fnu,
+                                     device=W.device)
+                dsmoe_q8_quantize_weights(self.handle, E, N, K, W, values, scales)
+                W = (values, scales)
+            if W is not None:
+                self.q[name] = tuple(W)
+        self._weights = DsmoeQ8Weights(*[_ptr(t) for n in Q8_WEIGHTS for t in self.q.get(n, (None, None))])
+
+    def alloc_rows(self, T: int):
+        """Buffers of T 8-bit rows: values [T, d], scales [T, S(d)]."""
+        import torch
+        dev, d = torch.device("cuda", self.device), self.cfg.d_model
+        return (torch.empty((T, d), dtype=torch.float8_e4m3fn, device=dev),
+                torch.empty((T, dsmoe_q8_scale_cols(d)), dtype=torch.float8_e8m0fnu, device=dev))
+
+    def forward(self, x, token_ids=None, out=None, with_scores: bool = False, stream=None, residual=None, x_q=None):
+        """The layer on x; x_q: its 8-bit rows (values, scales) where the caller has them (else they
+        are made here); residual: what the layer's output is added to in place of x."""
+        T = x.shape[0]
+        o = self.alloc_outputs(T, with_scores) if out is None else out
+        if x_q is None:
+            x_q = self.alloc_rows(T)
+            dsmoe_q8_quantize(self.handle, T, self.cfg.d_model, x, *x_q, stream)
+        w = self.w
+        dsmoe_forward_q8(self.handle, T, x, *x_q, residual, token_ids, w.get("W_router"), w.get("b"), self._weights,
+                         o["h"], o["topk_idx"], o["gates"], o["counts"], o["f"], o["P"], o["P_sum"], o["scores"],
+                         stream)
+        return o
+
+    def forward_norm(self, x, residual, w, eps: float, token_ids=None, with_scores: bool = False, stream=None):
+        """A block: r = x + residual, u = RMSNorm(r) w, h = r + the layer's experts on u. Returns the
+        layer's outputs and "r", "u"."""
+        import torch
+        T = x.shape[0]
+        r, u, x_q = torch.empty_like(x), torch.empty_like(x), self.alloc_rows(T)
+        dsmoe_norm_q8(self.handle, T, x, residual, w, eps, r, u, *x_q, stream)
+        o = self.forward(u, token_ids, None, with_scores, stream, r, x_q)
+        o["r"], o["u"] = r, u
         return o

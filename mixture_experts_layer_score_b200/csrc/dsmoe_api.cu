@@ -667,12 +667,10 @@ dsmoe_status route_stage(dsmoe_handle* h, const FwdArgs& a, cudaStream_t s, int*
   return DSMOE_OK;
 }
 
-// Counts, f, P (and P_sum), the slot offsets of the experts in [e0, e1), and the
-// permutation + gather of the token rows into h->Xp.
-dsmoe_status scan_permute_stage(dsmoe_handle* h, const FwdArgs& a, cudaStream_t s, int sel_grid, int e0, int e1,
-                                const std::function<cudaError_t(int)>& mark) {
+// Counts, f, P (and P_sum) and the slot offsets of the experts in [e0, e1).
+dsmoe_status scan_stage(dsmoe_handle* h, const FwdArgs& a, cudaStream_t s, int sel_grid, int e0, int e1) {
   const dsmoe_cfg& c = h->cfg;
-  const int T = a.T, N = c.n_routed, K = h->k_active, d = c.d_model;
+  const int T = a.T, N = c.n_routed, K = h->k_active;
   dsmoe::ScanArgs sc;
   sc.counts_ws = h->counts_ws;
   sc.P_part = c.score == DSMOE_ROUTE_HASH ? nullptr : h->P_part;
@@ -690,6 +688,16 @@ dsmoe_status scan_permute_stage(dsmoe_handle* h, const FwdArgs& a, cudaStream_t 
   sc.e_end = e1;
   CUDA_TRY(dsmoe::launch_scan_stats(sc, s));
   h->launches += 1;
+  return DSMOE_OK;
+}
+
+// The scan, and the permutation + gather of the token rows into h->Xp.
+dsmoe_status scan_permute_stage(dsmoe_handle* h, const FwdArgs& a, cudaStream_t s, int sel_grid, int e0, int e1,
+                                const std::function<cudaError_t(int)>& mark) {
+  const dsmoe_cfg& c = h->cfg;
+  const int T = a.T, N = c.n_routed, K = h->k_active, d = c.d_model;
+  const dsmoe_status st = scan_stage(h, a, s, sel_grid, e0, e1);
+  if (st != DSMOE_OK) return st;
   CUDA_TRY(mark(3));
   CUDA_TRY(dsmoe::launch_permute_gather(static_cast<const bf16*>(a.x), a.topk_idx, h->offsets, h->cursor, T, K, N,
                                         e0, e1, d, h->slot_of, h->Xp, h->status, h->num_sms, s));
@@ -1886,26 +1894,40 @@ dsmoe_status check_q8_dims(int64_t R, int32_t E, int32_t N, int32_t K, int n_ste
   return DSMOE_OK;
 }
 
-dsmoe_status q8_matmul(dsmoe_handle* h, int32_t E, int64_t R, int32_t N, int32_t K, const int32_t* offsets,
-                       const void* a, const void* a_scales, const void* W, const void* W_scales, const void* W1,
-                       const void* W1_scales, void* out, void* q_out, void* q_scales, cudaStream_t s) {
+// One grouped product: 8-bit rows and weights (W1: the up projection of a gated product), and
+// the output that `out` names.
+struct Q8Rows {
+  const void *values, *scales;
+};
+struct Q8Out {
+  void* bf16 = nullptr;              // [R, N]
+  void *q = nullptr, *scales = nullptr;
+  float* f32 = nullptr;              // [R, N] = add_bf16 + the product, or itself + the product
+  const void* add_bf16 = nullptr;
+};
+dsmoe_status q8_product(dsmoe_handle* h, int32_t E, int64_t R, int32_t N, int32_t K, const int32_t* offsets,
+                        const Q8Rows& a, const Q8Rows& W, const Q8Rows* W1, const Q8Out& out, cudaStream_t s) {
   dsmoe::Q8GemmArgs g;
   memset(&g, 0, sizeof(g));
-  const int tok = dsmoe::q8_token_tile(R, E, K);
-  if (!map_bytes(&g.map_a, a, K, R, 1, dsmoe::q8_box_rows(tok)) || !(W1 ? map_bytes(&g.map_w0, W, K, N, E, 128, true) && map_bytes(&g.map_w1, W1, K, N, E, 128, true)
-           : map_bytes_pairs(&g.map_w0, W, K, N, E)))
+  int tok = dsmoe::q8_token_tile(R, E, N, K, W1 != nullptr, h->num_sms);
+  if (out.f32) tok = std::min(tok, 112);
+  if (!map_bytes(&g.map_a, a.values, K, R, 1, dsmoe::q8_box_rows(tok)) ||
+      !(W1 ? map_bytes(&g.map_w0, W.values, K, N, E, 128, true) && map_bytes(&g.map_w1, W1->values, K, N, E, 128, true)
+           : map_bytes_pairs(&g.map_w0, W.values, K, N, E)))
     return fail(DSMOE_ERR_CUDA, "cuTensorMapEncodeTiled rejected a tensor map of this call");
-  g.a_scales = static_cast<const uint8_t*>(a_scales);
-  g.W_scales = static_cast<const uint8_t*>(W_scales);
-  g.W1_scales = static_cast<const uint8_t*>(W1_scales);
+  g.a_scales = static_cast<const uint8_t*>(a.scales);
+  g.W_scales = static_cast<const uint8_t*>(W.scales);
+  g.W1_scales = W1 ? static_cast<const uint8_t*>(W1->scales) : nullptr;
   g.offsets = offsets;
   g.E = E;
   g.R = static_cast<int>(R);
   g.N = N;
   g.K = K;
-  g.out = static_cast<bf16*>(out);
-  g.q_out = static_cast<uint8_t*>(q_out);
-  g.q_scales = static_cast<uint8_t*>(q_scales);
+  g.out = static_cast<bf16*>(out.bf16);
+  g.q_out = static_cast<uint8_t*>(out.q);
+  g.q_scales = static_cast<uint8_t*>(out.scales);
+  g.out_f32 = out.f32;
+  g.add_bf16 = static_cast<const bf16*>(out.add_bf16);
   g.status = h->status;
   g.wait_limit_ns = h->wait_ns;
   CUDA_TRY(dsmoe::launch_gemm_q8(g, tok, h->num_sms, s));
@@ -2013,13 +2035,15 @@ DSMOE_EXPORT dsmoe_status dsmoe_q8_matmul(dsmoe_handle* h, int32_t E, int64_t R,
                                           const void* W_scales, void* out, void* stream) {
   if (!h) return fail(DSMOE_ERR_INVALID_ARG, "handle is NULL");
   STAGE_TRY(check_q8_dims(R, E, N, K, 8));
-  if (!offsets) return fail(DSMOE_ERR_INVALID_ARG, "offsets is required");
+  if (!offsets && E != 1) return fail(DSMOE_ERR_INVALID_ARG, "offsets is required for E = %d", E);
   if (R == 0) return DSMOE_OK;
   STAGE_TRY(check_pointers({a, a_scales, W, W_scales, out}));
   DeviceGuard g(h->device);
   if (!g.ok) return fail(DSMOE_ERR_CUDA, "cannot select device %d", h->device);
-  return q8_matmul(h, E, R, N, K, offsets, a, a_scales, W, W_scales, nullptr, nullptr, out, nullptr, nullptr,
-                   static_cast<cudaStream_t>(stream));
+  Q8Out o;
+  o.bf16 = out;
+  return q8_product(h, E, R, N, K, offsets, {a, a_scales}, {W, W_scales}, nullptr, o,
+                    static_cast<cudaStream_t>(stream));
 }
 
 DSMOE_EXPORT dsmoe_status dsmoe_q8_gated_matmul(dsmoe_handle* h, int32_t E, int64_t R, int32_t N, int32_t K,
@@ -2028,11 +2052,142 @@ DSMOE_EXPORT dsmoe_status dsmoe_q8_gated_matmul(dsmoe_handle* h, int32_t E, int6
                                                 const void* up_scales, void* q, void* scales, void* stream) {
   if (!h) return fail(DSMOE_ERR_INVALID_ARG, "handle is NULL");
   STAGE_TRY(check_q8_dims(R, E, N, K, 16));
-  if (!offsets) return fail(DSMOE_ERR_INVALID_ARG, "offsets is required");
+  if (!offsets && E != 1) return fail(DSMOE_ERR_INVALID_ARG, "offsets is required for E = %d", E);
   if (R == 0) return DSMOE_OK;
   STAGE_TRY(check_pointers({a, a_scales, W_gate, gate_scales, W_up, up_scales, q, scales}));
   DeviceGuard g(h->device);
   if (!g.ok) return fail(DSMOE_ERR_CUDA, "cannot select device %d", h->device);
-  return q8_matmul(h, E, R, N, K, offsets, a, a_scales, W_gate, gate_scales, W_up, up_scales, nullptr, q, scales,
-                   static_cast<cudaStream_t>(stream));
+  const Q8Rows up{W_up, up_scales};
+  Q8Out o;
+  o.q = q;
+  o.scales = scales;
+  return q8_product(h, E, R, N, K, offsets, {a, a_scales}, {W_gate, gate_scales}, &up, o,
+                    static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+struct FwdQ8Args {
+  FwdArgs f;  // the routing half; its expert weights stay NULL
+  const void *xq, *xs, *residual;
+  const dsmoe_q8_weights* w;
+};
+
+dsmoe_status check_forward_q8(dsmoe_handle* h, const FwdQ8Args& a) {
+  dsmoe_status st = check_route(h, a.f);
+  if (st != DSMOE_OK || a.f.T == 0) return st;
+  if (!a.w) return fail(DSMOE_ERR_INVALID_ARG, "weights is NULL");
+  const dsmoe_q8_weights& w = *a.w;
+  st = check_pointers({a.xq, a.xs, a.f.h, w.W_gate, w.W_gate_scales, w.W_up, w.W_up_scales, w.W_down, w.W_down_scales});
+  if (st == DSMOE_OK && h->add_shared && h->cfg.n_shared > 0)
+    st = check_pointers({w.Ws_gate, w.Ws_gate_scales, w.Ws_up, w.Ws_up_scales, w.Ws_down, w.Ws_down_scales});
+  if (st != DSMOE_OK) return st;
+  if (a.residual && !aligned16(a.residual))
+    return fail(DSMOE_ERR_INVALID_ARG, "pointer %p is not 16-byte aligned", a.residual);
+  return DSMOE_OK;
+}
+
+// Shared expert i of 8-bit weights [K_s, N, K].
+Q8Rows shared_weight(const void* values, const void* scales, int i, int64_t N, int64_t K) {
+  const int64_t sb = (N + 127) / 128 * dsmoe::q8_scale_cols(static_cast<int>(K));
+  return {static_cast<const char*>(values) + i * N * K, static_cast<const char*>(scales) + i * sb};
+}
+
+// The forward's stages with 8-bit rows: Xp, A1 and A1s hold [values | scales].
+dsmoe_status run_forward_q8(dsmoe_handle* h, const FwdQ8Args& q, cudaStream_t s) {
+  const dsmoe_cfg& c = h->cfg;
+  const FwdArgs& a = q.f;
+  const dsmoe_q8_weights& w = *q.w;
+  const int T = a.T, N = c.n_routed, K = h->k_active, d = c.d_model, F = c.d_ff, Fs = c.d_ff_shared;
+  const int Ks = h->add_shared ? c.n_shared : 0, e0 = h->e_begin, NL = h->e_end - h->e_begin;
+  const int64_t R = static_cast<int64_t>(T) * K;
+  cudaEvent_t* evs = h->ev[h->timed_forwards % kTimingSlots];
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (h->timing) CUDA_TRY(cudaStreamIsCapturing(s, &cap));
+  const unsigned rec_flags = cap == cudaStreamCaptureStatusActive ? cudaEventRecordExternal : cudaEventRecordDefault;
+  const auto mark_on = [&](int i, cudaStream_t st) -> cudaError_t {
+    return h->timing ? cudaEventRecordWithFlags(evs[i], st, rec_flags) : cudaSuccess;
+  };
+  const std::function<cudaError_t(int)> mark = [&](int i) { return mark_on(i, s); };
+
+  // the workspace no longer holds a training forward's rows or an expert-parallel slot table
+  h->saved_T = -1;
+  h->dab_ready = false;
+  h->ep_T = -1;
+  CUDA_TRY(mark(0));
+  if (Ks > 0) {
+    CUDA_TRY(cudaEventRecord(h->ev_fork, s));
+    CUDA_TRY(cudaStreamWaitEvent(h->side, h->ev_fork, 0));
+  }
+  int sel_grid = 0;
+  STAGE_TRY(route_stage(h, a, s, &sel_grid, mark));
+  const void* base = q.residual ? q.residual : a.x;
+  if (Ks > 0) {
+    CUDA_TRY(mark_on(kChainStages + 1, h->side));
+    const Q8Rows x{q.xq, q.xs}, m{h->A1s, reinterpret_cast<char*>(h->A1s) + static_cast<int64_t>(T) * Fs};
+    for (int i = 0; i < Ks; ++i) {
+      const Q8Rows up = shared_weight(w.Ws_up, w.Ws_up_scales, i, Fs, d);
+      Q8Out o;
+      o.q = const_cast<void*>(m.values);
+      o.scales = const_cast<void*>(m.scales);
+      STAGE_TRY(q8_product(h, 1, T, Fs, d, nullptr, x, shared_weight(w.Ws_gate, w.Ws_gate_scales, i, Fs, d), &up, o,
+                           h->side));
+      Q8Out o2;
+      o2.f32 = h->Hs;
+      o2.add_bf16 = i == 0 ? base : nullptr;
+      STAGE_TRY(q8_product(h, 1, T, d, Fs, nullptr, m, shared_weight(w.Ws_down, w.Ws_down_scales, i, d, Fs), nullptr,
+                           o2, h->side));
+    }
+    CUDA_TRY(mark_on(kChainStages + 2, h->side));
+    CUDA_TRY(cudaEventRecord(h->ev_join, h->side));
+  }
+  CUDA_TRY(mark(2));
+  STAGE_TRY(scan_stage(h, a, s, sel_grid, e0, e0 + NL));
+  CUDA_TRY(mark(3));
+  uint8_t* xp = reinterpret_cast<uint8_t*>(h->Xp);
+  uint8_t* a1 = reinterpret_cast<uint8_t*>(h->A1);
+  uint8_t *xp_s = xp + R * d, *a1_s = a1 + R * F;
+  CUDA_TRY(dsmoe::launch_permute_q8(static_cast<const uint8_t*>(q.xq), static_cast<const uint8_t*>(q.xs), a.topk_idx,
+                                    h->offsets, h->cursor, T, K, N, e0, e0 + NL, d, h->slot_of, xp, xp_s, h->status,
+                                    h->num_sms, s));
+  h->launches += 1;
+  CUDA_TRY(mark(4));
+  const Q8Rows up{w.W_up, w.W_up_scales};
+  Q8Out o;
+  o.q = a1;
+  o.scales = a1_s;
+  STAGE_TRY(q8_product(h, NL, R, F, d, h->offsets + e0, {xp, xp_s}, {w.W_gate, w.W_gate_scales}, &up, o, s));
+  CUDA_TRY(mark(5));
+  Q8Out o2;
+  o2.bf16 = h->Y;
+  STAGE_TRY(q8_product(h, NL, R, d, F, h->offsets + e0, {a1, a1_s}, {w.W_down, w.W_down_scales}, nullptr, o2, s));
+  CUDA_TRY(mark(6));
+  if (Ks > 0) CUDA_TRY(cudaStreamWaitEvent(s, h->ev_join, 0));
+  FwdArgs fc = a;
+  fc.x = base;
+  STAGE_TRY(combine_stage(h, fc, h->Y, Ks, h->add_shared, h->partial, s));
+  CUDA_TRY(mark(7));
+  if (Ks == 0) {
+    CUDA_TRY(mark(kChainStages + 1));
+    CUDA_TRY(mark(kChainStages + 2));
+  }
+  if (h->timing) h->timed_forwards += 1;
+  return DSMOE_OK;
+}
+}  // namespace
+
+DSMOE_EXPORT dsmoe_status dsmoe_forward_q8(dsmoe_handle* h, int32_t T, const void* x, const void* x_q,
+                                           const void* x_scales, const void* residual, const int32_t* token_ids,
+                                           const void* W_router, const float* b, const dsmoe_q8_weights* weights,
+                                           void* h_out, int32_t* topk_idx, float* gates, int32_t* counts, float* f,
+                                           float* P, float* P_sum, float* scores_dbg, void* stream) {
+  if (!h) return fail(DSMOE_ERR_INVALID_ARG, "handle is NULL");
+  FwdQ8Args q{FwdArgs{T, x, W_router, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, token_ids, b, h_out,
+                      topk_idx, gates, counts, f, P, P_sum, scores_dbg},
+              x_q, x_scales, residual, weights};
+  STAGE_TRY(check_forward_q8(h, q));
+  DeviceGuard g(h->device);
+  if (!g.ok) return fail(DSMOE_ERR_CUDA, "cannot select device %d", h->device);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0) return zero_stats(q.f, h->cfg.n_routed, s);
+  return run_forward_q8(h, q, s);
 }

@@ -308,6 +308,13 @@ cudaError_t launch_quantize_rows(const bf16* x, int64_t R, int C, uint8_t* q, ui
 cudaError_t launch_quantize_weights(const bf16* W, int E, int N, int K, uint8_t* q, uint8_t* scales, int num_sms,
                                     cudaStream_t s);
 
+// The 8-bit rows' permutation: as launch_permute_gather, for values [T, d] and scales
+// [T, q8_scale_cols(d)] into expert-contiguous order.
+cudaError_t launch_permute_q8(const uint8_t* q, const uint8_t* scales, const int32_t* topk_idx,
+                              const int32_t* offsets, int32_t* cursor, int T, int K, int N, int e_begin, int e_end,
+                              int d, int32_t* slot_of, uint8_t* q_out, uint8_t* scales_out, uint32_t* status,
+                              int num_sms, cudaStream_t s);
+
 // r = bf16(x + residual) (x without one), u = bf16(r rsqrt(mean(r^2) + eps) w), q8 of u.
 struct NormArgs {
   const bf16* x;
@@ -348,7 +355,7 @@ struct Q8GemmArgs {
   const uint8_t* a_scales;   // [R, q8_scale_cols(K)]
   const uint8_t* W_scales;   // [E, ceil(N / 128), q8_scale_cols(K)]
   const uint8_t* W1_scales;
-  const int32_t* offsets;    // [E + 1]
+  const int32_t* offsets;    // [E + 1], or nullptr: E = 1, all rows
   int E, R, N, K;
   bf16* out;                 // [R, N]
   uint8_t* q_out;            // [R, N]
@@ -359,8 +366,8 @@ struct Q8GemmArgs {
   uint64_t wait_limit_ns;
 };
 // Tokens per tile for R rows over E groups, and the row box of map_a: a tile copies the
-// boxes that hold its rows.
-int q8_token_tile(int64_t R, int E, int K);
+// boxes that hold its rows. (The fp32 output takes tiles of at most 112.)
+int q8_token_tile(int64_t R, int E, int N, int K, bool gated, int num_sms);
 constexpr int q8_box_rows(int tok) { return tok == 240 ? 48 : tok == 112 ? 56 : 16; }
 cudaError_t launch_gemm_q8(const Q8GemmArgs& a, int tok, int num_sms, cudaStream_t s);
 

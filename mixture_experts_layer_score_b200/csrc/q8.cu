@@ -119,6 +119,57 @@ __global__ void __launch_bounds__(256, 4) quantize_weights_kernel(const bf16* __
   }
 }
 
+// One warp per token: lanes k < K' claim a slot in their expert's segment (experts in
+// [e_begin, e_end); the others get slot -1), then the warp copies the token's 8-bit row
+// (16-byte vectors, four in flight per lane) and its scales (words) to each claimed slot.
+__global__ void __launch_bounds__(256) permute_q8_kernel(const uint8_t* __restrict__ q,
+                                                         const uint8_t* __restrict__ scales,
+                                                         const int32_t* __restrict__ topk_idx,
+                                                         const int32_t* __restrict__ offsets,
+                                                         int32_t* __restrict__ cursor, int T, int K, int N,
+                                                         int e_begin, int e_end, int d,
+                                                         int32_t* __restrict__ slot_of, uint8_t* __restrict__ q_out,
+                                                         uint8_t* __restrict__ scales_out, uint32_t* status) {
+  const int lane = threadIdx.x & 31;
+  const int gw = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, nw = (gridDim.x * blockDim.x) >> 5;
+  const int d16 = d >> 4, S4 = q8_scale_cols(d) >> 2;
+  for (int t = gw; t < T; t += nw) {
+    int pos = -1;
+    if (lane < K) {
+      const int e = topk_idx[static_cast<int64_t>(t) * K + lane];
+      if (e < 0 || e >= N) {
+        atomicOr(status, kStatusBadIndex);
+      } else if (e >= e_begin && e < e_end) {
+        pos = offsets[e] + atomicAdd(&cursor[e], 1);
+      }
+      slot_of[static_cast<int64_t>(t) * K + lane] = pos;
+    }
+    int pk[16];  // every lane learns all K' slots (K' <= 16)
+#pragma unroll
+    for (int k = 0; k < 16; ++k) pk[k] = __shfl_sync(0xffffffffu, pos, k);
+    const uint4* src = reinterpret_cast<const uint4*>(q) + static_cast<int64_t>(t) * d16;
+    for (int c0 = lane; c0 < d16; c0 += 4 * 32) {
+      uint4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (c0 + 32 * u < d16) v[u] = src[c0 + 32 * u];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (c0 + 32 * u < d16)
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (k < K && pk[k] >= 0)
+              reinterpret_cast<uint4*>(q_out)[static_cast<int64_t>(pk[k]) * d16 + c0 + 32 * u] = v[u];
+    }
+    for (int c = lane; c < S4; c += 32) {
+      const uint32_t v = reinterpret_cast<const uint32_t*>(scales)[static_cast<int64_t>(t) * S4 + c];
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        if (k < K && pk[k] >= 0) reinterpret_cast<uint32_t*>(scales_out)[static_cast<int64_t>(pk[k]) * S4 + c] = v;
+    }
+  }
+}
+
 // Sums of n values over the block, in a fixed order (warp butterflies, then the warps' sums in
 // order); every thread gets them. red holds 32 n floats that the block has zeroed once; two
 // of them used in turn make one barrier per call enough.
@@ -423,6 +474,16 @@ cudaError_t launch_quantize_weights(const bf16* W, int E, int N, int K, uint8_t*
   if (grid > tiles) grid = tiles;
   if (grid < 1) return cudaSuccess;
   quantize_weights_kernel<<<static_cast<int>(grid), 256, 0, s>>>(W, tiles, N, K, q, scales);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_permute_q8(const uint8_t* q, const uint8_t* scales, const int32_t* topk_idx,
+                              const int32_t* offsets, int32_t* cursor, int T, int K, int N, int e_begin, int e_end,
+                              int d, int32_t* slot_of, uint8_t* q_out, uint8_t* scales_out, uint32_t* status,
+                              int num_sms, cudaStream_t s) {
+  const int grid = std::max(1, std::min((T + 7) / 8, 8 * num_sms));
+  permute_q8_kernel<<<grid, 256, 0, s>>>(q, scales, topk_idx, offsets, cursor, T, K, N, e_begin, e_end, d, slot_of,
+                                         q_out, scales_out, status);
   return cudaGetLastError();
 }
 

@@ -19,6 +19,8 @@ def test_scale_cols():
     lambda: M.dsmoe_norm_backward(None, 1, 16, None, 16, 16, 1e-6, 16, 16, 0),
     lambda: M.dsmoe_q8_matmul(None, 1, 1, 8, 16, 16, 16, 16, 16, 16, 16, 0),
     lambda: M.dsmoe_q8_gated_matmul(None, 1, 1, 16, 16, 16, 16, 16, 16, 16, 16, 16, 16, 16, 0),
+    lambda: M.dsmoe_forward_q8(None, 1, 16, 16, 16, None, None, 16, None, M.DsmoeQ8Weights(), 16, 16, 16, 16, 16, 16,
+                               None, None, 0),
 ])
 def test_a_null_handle_is_refused(call):
     with pytest.raises(M.DsmoeError) as e:
@@ -97,11 +99,11 @@ class TestHandle:
 
     def test_product_pointers(self):
         for i in range(6):
-            for bad in ((None, 8) if i else (None,)):
+            for bad in ((None, 8) if i else (None,)):  # (offsets may only be NULL where E is 1)
                 p = [16] * 6
                 p[i] = bad
-                assert self.status(lambda: M.dsmoe_q8_matmul(self.h, 1, 1, 8, 16, *p, 0)) == 1
+                assert self.status(lambda: M.dsmoe_q8_matmul(self.h, 2, 1, 8, 16, *p, 0)) == 1
         for i in range(9):
             p = [16] * 9
             p[i] = None
-            assert self.status(lambda: M.dsmoe_q8_gated_matmul(self.h, 1, 1, 16, 16, *p, 0)) == 1
+            assert self.status(lambda: M.dsmoe_q8_gated_matmul(self.h, 2, 1, 16, 16, *p, 0)) == 1
