@@ -428,7 +428,7 @@ def _take(where: str, handle, stream, *tensors):
     kinds = _DTYPES or (_dtypes("bf16"), _DTYPES)[1]
     ptrs = []
     for name, t, kind, n in tensors:
-        if t is None or isinstance(t, int):
+        if t is None or t.__class__ is int:
             ptrs.append(t)
             continue
         if t.dtype not in kinds[kind] or t.numel() != n or not t.is_contiguous() or \
@@ -485,8 +485,9 @@ def dsmoe_norm_q8(handle, T, x, residual, w, eps, r, u, q, scales, stream=None) 
     d = _norm_width(where, handle, w)
     n = T * d
     (x, residual, w, r, u, q, scales), s = _take(
-        where, handle, stream, ("x", x, "bf16", n), ("residual", residual, "bf16", n), ("w", w, "bf16", d), ("r", r, "bf16", n),
-        ("u", u, "bf16", n), ("q", q, "q8", n), ("scales", scales, "q8", T * dsmoe_q8_scale_cols(d)))
+        where, handle, stream, ("x", x, "bf16", n), ("residual", residual, "bf16", n), ("w", w, "bf16", d),
+        ("r", r, "bf16", n), ("u", u, "bf16", n), ("q", q, "q8", n),
+        ("scales", scales, "q8", T * dsmoe_q8_scale_cols(d)))
     _check(_lib.dsmoe_norm_q8(handle, T, x, residual, w, float(eps), r, u, q, scales, s), where)
 
 
@@ -494,16 +495,19 @@ def dsmoe_norm_backward(handle, T, dy, dres, r, w, eps, dx, dw, stream=None) -> 
     where, T = "dsmoe_norm_backward", int(T)
     d = _norm_width(where, handle, w)
     n = T * d
-    (dy, dres, r, w, dx, dw), s = _take(where, handle, stream, ("dy", dy, "f32", n), ("dres", dres, "bf16", n), ("r", r, "bf16", n),
-                                        ("w", w, "bf16", d), ("dx", dx, "bf16", n), ("dw", dw, "f32", d))
+    (dy, dres, r, w, dx, dw), s = _take(
+        where, handle, stream, ("dy", dy, "f32", n), ("dres", dres, "bf16", n), ("r", r, "bf16", n),
+        ("w", w, "bf16", d), ("dx", dx, "bf16", n), ("dw", dw, "f32", d))
     _check(_lib.dsmoe_norm_backward(handle, T, dy, dres, r, w, float(eps), dx, dw, s), where)
 
 
 def dsmoe_q8_matmul(handle, E, R, N, K, offsets, a, a_scales, W, W_scales, out, stream=None) -> None:
     where, E, R, N, K = "dsmoe_q8_matmul", int(E), int(R), int(N), int(K)
     S = dsmoe_q8_scale_cols(K)
-    p, s = _take(where, handle, stream, ("offsets", offsets, "i32", E + 1), ("a", a, "q8", R * K), ("a_scales", a_scales, "q8", R * S),
-                 ("W", W, "q8", E * N * K), ("W_scales", W_scales, "q8", E * -(-N // 128) * S), ("out", out, "bf16", R * N))
+    p, s = _take(
+        where, handle, stream, ("offsets", offsets, "i32", E + 1), ("a", a, "q8", R * K),
+        ("a_scales", a_scales, "q8", R * S), ("W", W, "q8", E * N * K),
+        ("W_scales", W_scales, "q8", E * -(-N // 128) * S), ("out", out, "bf16", R * N))
     _check(_lib.dsmoe_q8_matmul(handle, E, R, N, K, *p, s), where)
 
 
@@ -512,9 +516,11 @@ def dsmoe_q8_gated_matmul(handle, E, R, N, K, offsets, a, a_scales, W_gate, gate
     where, E, R, N, K = "dsmoe_q8_gated_matmul", int(E), int(R), int(N), int(K)
     S = dsmoe_q8_scale_cols(K)
     nw, ns = E * N * K, E * -(-N // 128) * S
-    p, s = _take(where, handle, stream, ("offsets", offsets, "i32", E + 1), ("a", a, "q8", R * K), ("a_scales", a_scales, "q8", R * S),
-                 ("W_gate", W_gate, "q8", nw), ("gate_scales", gate_scales, "q8", ns), ("W_up", W_up, "q8", nw),
-                 ("up_scales", up_scales, "q8", ns), ("q", q, "q8", R * N), ("scales", scales, "q8", R * dsmoe_q8_scale_cols(N)))
+    p, s = _take(
+        where, handle, stream, ("offsets", offsets, "i32", E + 1), ("a", a, "q8", R * K),
+        ("a_scales", a_scales, "q8", R * S), ("W_gate", W_gate, "q8", nw), ("gate_scales", gate_scales, "q8", ns),
+        ("W_up", W_up, "q8", nw), ("up_scales", up_scales, "q8", ns), ("q", q, "q8", R * N),
+        ("scales", scales, "q8", R * dsmoe_q8_scale_cols(N)))
     _check(_lib.dsmoe_q8_gated_matmul(handle, E, R, N, K, *p, s), where)
 
 

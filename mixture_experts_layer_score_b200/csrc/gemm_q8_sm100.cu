@@ -22,18 +22,23 @@
 //   warps 2-9   epilogue: two groups of four warps take alternate 8-token chunks; warp q of
 //               a group reads TMEM lanes [32q, 32q+32) into registers and frees the
 //               accumulator; the group then transposes two chunks at a time through shared
-//               memory so that each output row leaves in one coalesced store. 128 features are one scale block, so the gated output's maximum over
-//               a block is a maximum over the row of the staged chunk.
+//               memory so that each output row leaves in one coalesced store. 128
+//               features are one scale block, so the gated output's maximum over a block
+//               is one over a row of the staged chunk.
 //   warp 10     scale loader: a 32-bit word of a row's scales is four K blocks; the words
 //               of the tile's tokens and of the two weight tiles go to a ring of slots
 //               in the layout that the copy into tensor memory takes.
 // Every wait is bounded; a role that gives up raises the abort flag and a status bit, the
-// CTA drains its copies and MMAs and returns. The epilogue's groups decide together
-// (through shared memory), so that none of their barriers is left waiting.
+// CTA drains its copies and MMAs and returns; the epilogue's groups decide together (through
+// shared memory), so that none of their barriers is left waiting. Where a launch has few tiles (few rows, few
+// features), the CTAs of a cluster share a tile along K: each sends its fp32 partial sums
+// through distributed shared memory to the CTA that owns the token, which adds them in the
+// order of K.
 #include <algorithm>
 
 #include "kernels.h"
 #include "q8.cuh"
+#include "sm100_pair_ptx.cuh"
 #include "sm100_ptx.cuh"
 
 namespace dsmoe {
@@ -139,6 +144,16 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// mbar_wait_bounded that looks at the limit after every poll.
+__device__ __forceinline__ bool mbar_wait_checked(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
+                                                  volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (*abort_flag || global_timer_ns() - t0 > limit_ns) return false;
+  return true;
+}
+
 // mbar_wait_bounded for a converged warp: every lane polls, the decisions are the warp's.
 __device__ __forceinline__ bool mbar_wait_converged(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
                                                     volatile int* abort_flag) {
@@ -188,7 +203,36 @@ __device__ __forceinline__ Q8Tile decode_tile(const Q8GemmArgs& a, const int32_t
   return t;
 }
 
-template <int kOut, int kTok>
+__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+
+// The warp stores one row's block of 128 gated outputs in 8 bits, four features per lane, and
+// its scale (the last block of a row also the row's padding scales).
+__device__ __forceinline__ void store_gated_row(const Q8GemmArgs& a, int64_t row, int blk, int lane, const float4& m) {
+  const int So = q8_scale_cols(a.N), nb = (a.N + kFeat - 1) / kFeat, f = blk * kFeat + 4 * lane;
+  const uint32_t s = q8_scale_byte(__reduce_max_sync(
+      0xffffffffu, max(max(abs_bits(m.x), abs_bits(m.y)), max(abs_bits(m.z), abs_bits(m.w)))));
+  const float k = q8_inv_scale(s);
+  if (f < a.N)
+    *reinterpret_cast<uint32_t*>(a.q_out + row * a.N + f) =
+        s == 255u ? 0x7F7F7F7Fu : q8_pack4(m.x * k, m.y * k, m.z * k, m.w * k);
+  if (lane == 0) a.q_scales[row * So + blk] = static_cast<uint8_t>(s);
+  if (blk == nb - 1 && lane < So - nb) a.q_scales[row * So + nb + lane] = kQ8PadScale;
+}
+
+// Four fp32 outputs at `at`: added to the bf16 rows given, or to what is there.
+__device__ __forceinline__ void add_f32(const Q8GemmArgs& a, int64_t at, float4 o) {
+  if (a.add_bf16) {
+    const uint2 x = *reinterpret_cast<const uint2*>(a.add_bf16 + at);
+    const float2 x0 = unpack_bf16x2(x.x), x1 = unpack_bf16x2(x.y);
+    o.x += x0.x, o.y += x0.y, o.z += x1.x, o.w += x1.y;
+  } else {
+    const float4 x = *reinterpret_cast<const float4*>(a.out_f32 + at);
+    o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+  }
+  *reinterpret_cast<float4*>(a.out_f32 + at) = o;
+}
+
+template <int kOut, int kTok, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_constant__ Q8GemmArgs a) {
   using G_ = Geo<kTok>;
   constexpr bool kGated = kOut == kOutGated;
@@ -216,7 +260,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_tiles = (a.N + kTileFeat - 1) / kTileFeat;
-  const int kb_n = (a.K + kBK - 1) / kBK, kq_n = (kb_n + 3) >> 2;
+  const int kb_all = (a.K + kBK - 1) / kBK, kq_all = (kb_all + 3) >> 2;
+  // kSplit: the CTAs of a cluster share one tile, each a range of K in whole groups of four blocks
+  const int splits = kSplit ? a.splits : 1, rank = kSplit ? static_cast<int>(pair::cta_rank()) : 0;
+  const int kq0 = kSplit ? rank * kq_all / splits : 0, kq1 = kSplit ? (rank + 1) * kq_all / splits : kq_all;
+  const int kb0 = 4 * kq0, kb1 = kSplit ? min(4 * kq1, kb_all) : kb_all;
+  const int tile0 = kSplit ? blockIdx.x / splits : blockIdx.x, tile_step = kSplit ? gridDim.x / splits : gridDim.x;
 
   for (int e = threadIdx.x; e < a.E; e += kThreads) {
     int b, t;
@@ -264,6 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (kSplit) pair::cluster_sync();  // every CTA of the cluster is there to be written to
   const uint32_t tmem_base = *tmem_slot;
   const int total = tile_start[a.E];
 
@@ -275,14 +325,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+      for (int tile = tile0; ok && tile < total; tile += tile_step) {
         const Q8Tile t = decode_tile<kTok>(a, tile_start, tile);
         const int n0 = t.n_blk * kTileFeat;
         // only the boxes that hold rows of the tile: the copies into shared memory are what
         // bounds the large products
         const int boxes = (t.m_valid + G_::kBoxRows - 1) / G_::kBoxRows;
         const uint32_t stage_bytes = kWBytes + boxes * G_::kBoxRows * kBK;
-        for (int kb = 0; kb < kb_n; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, a.wait_limit_ns, abort_flag)) {
             ok = false;
             break;
@@ -322,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
     uint32_t quad = 0;  // groups of four K blocks so far
     bool ok = true;
     int it = 0;
-    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x, ++it) {
+    for (int tile = tile0; ok && tile < total; tile += tile_step, ++it) {
       const Q8Tile t = decode_tile<kTok>(a, tile_start, tile);
       const int n_mma = (t.m_valid + 15) & ~15;
       const uint32_t idesc = idesc_q8(kFeat, n_mma, 0);
@@ -334,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
       tc_fence_after();
       const uint32_t d0 = tmem_base + acc * G_::kAccCols;
       uint32_t sf = 0;
-      for (int kb = 0; kb < kb_n; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         const uint32_t id = kb & 3;
         if (id == 0) {
           // the columns of this set were last read by the MMAs of two groups ago
@@ -369,16 +419,16 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
 #pragma unroll
           for (int k = 0; k < kBK / kMmaK; ++k) {
             const uint64_t dk = static_cast<uint64_t>(2 * k);
-            const uint32_t accum = (kb | k) ? 1u : 0u;
+            const uint32_t accum = (kb > kb0 || k) ? 1u : 0u;
             mma_q8_ss(d0, w0 + dk, xd + dk, di, sf, sf + 8, accum);
             mma_q8_ss(d0 + kTok, w1 + dk, xd + dk, di, kGated ? sf + 4 : sf, sf + 8, accum);
           }
           mma_commit(&empty[stage]);
-          if (id == 3 || kb == kb_n - 1) mma_commit(&sf_empty[quad % kSfSlots]);
-          if (kb == kb_n - 1) mma_commit(&acc_full[acc]);
+          if (id == 3 || kb == kb1 - 1) mma_commit(&sf_empty[quad % kSfSlots]);
+          if (kb == kb1 - 1) mma_commit(&acc_full[acc]);
         }
         __syncwarp();
-        if (id == 3 || kb == kb_n - 1) ++quad;
+        if (id == 3 || kb == kb1 - 1) ++quad;
         if (++stage == G_::kStages) {
           stage = 0;
           phase ^= 1u;
@@ -399,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
     constexpr int kWords = (kTok + 31) / 32;
     uint32_t quad = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+    for (int tile = tile0; ok && tile < total; tile += tile_step) {
       const Q8Tile t = decode_tile<kTok>(a, tile_start, tile);
       const int nb0 = kGated ? t.n_blk : 2 * t.n_blk, nb1 = kGated ? nb0 : nb0 + 1;
       const uint32_t* p0 = ws0 + (static_cast<int64_t>(t.expert) * nnb + nb0) * S4;
@@ -415,8 +465,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
             w[i] = __ldg(as + static_cast<int64_t>(t.row0 + 32 * i + lane) * S4 + kq);
         }
       };
-      load(0);
-      for (int kq = 0; kq < kq_n; ++kq, ++quad) {
+      load(kq0);
+      for (int kq = kq0; kq < kq1; ++kq, ++quad) {
         const uint32_t slot = quad % kSfSlots;
         if (!mbar_wait_warp(&sf_empty[slot], ((quad / kSfSlots) & 1u) ^ 1u, a.wait_limit_ns, abort_flag)) {
           ok = false;
@@ -433,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
         if (kTok > 128) dst[96] = make_uint4(w[4], w[5], w[6], w[7]);
         fence_proxy_async();
         mbar_arrive(&sf_full[slot]);
-        if (kq + 1 < kq_n) load(kq + 1);
+        if (kq + 1 < kq1) load(kq + 1);
       }
     }
     if (!ok && lane == 0) {
@@ -446,14 +496,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
     const bool leader = ((warp - 2) & 3) == 0 && lane == 0;
     uint8_t* stg = base + G_::kOffStg + half * 2 * kStgBytes;
     uint32_t buf = 0;  // staging buffer of the next chunk
-    const int So = kGated ? q8_scale_cols(a.N) : 0, nbo = (a.N + kFeat - 1) / kFeat;
     const int w4 = (warp - 2) & 3;  // this warp's rows of a staged chunk: 4 w4 .. 4 w4 + 3
     int it = 0;
-    for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++it) {
+    for (int tile = tile0; tile < total; tile += tile_step, ++it) {
       const Q8Tile t = decode_tile<kTok>(a, tile_start, tile);
       const int acc = it % G_::kBufs;
       if (leader) {
-        const bool ok = mbar_wait_bounded(&acc_full[acc], (it / G_::kBufs) & 1, a.wait_limit_ns, abort_flag);
+        const bool ok = mbar_wait_checked(&acc_full[acc], (it / G_::kBufs) & 1, a.wait_limit_ns, abort_flag);
         group_ok[2 * half + (it & 1)] = ok;
         if (!ok) {
           *abort_flag = 1;
@@ -468,100 +517,104 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * G_::kAccCols;
       const int n_chunks = (t.m_valid + kChunk - 1) / kChunk;
       const int n0 = t.n_blk * kTileFeat;
-      // First the accumulators move to registers (gated: through SwiGLU; bf16: both chains
-      // rounded into one register), so that the next tile's MMAs may overwrite them ...
-      uint32_t hold[kHold][kChunk], hold1[kOut == kOutF32 ? kHold : 1][kChunk];
-      uint32_t v0[2][kChunk], v1[2][kChunk];
+      if constexpr (kSplit) {
+        // the partial sums of token t go to CTA t % splits, slot t / splits, where part
+        // [source CTA][slot][chain][feature] of the staging area waits for them
 #pragma unroll
-      for (int i = 0; i < kHold; i += 2) {  // two chunks at a time
-        if (2 * i + half >= n_chunks) break;
-        const uint32_t at = tb + kChunk * (2 * i + half);
-        tmem_ld8(at, v0[0]);
-        tmem_ld8(at + kTok, v1[0]);
-        if (i + 1 < kHold) {  // (columns past the tile's tokens hold what nothing reads)
-          tmem_ld8(at + 2 * kChunk, v0[1]);
-          tmem_ld8(at + 2 * kChunk + kTok, v1[1]);
-        }
-        tmem_wait_ld();
+        for (int i = 0; i < kHold; ++i) {
+          const int c = 2 * i + half;
+          if (c >= n_chunks) break;
+          uint32_t p0[kChunk], p1[kChunk];
+          tmem_ld8(tb + kChunk * c, p0);
+          tmem_ld8(tb + kTok + kChunk * c, p1);
+          tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 2 * kChunk; ++j) {
-          const int s = j >= kChunk ? 1 : 0;
-          if (i + s >= kHold) break;
-          const uint32_t u = v0[s][j & 7], v = v1[s][j & 7];
-          const float x = __uint_as_float(u), y = __uint_as_float(v);
-          if (kGated) hold[i + s][j & 7] = __float_as_uint(__fdividef(x, 1.0f + __expf(-x)) * y);
-          else if (kOut == kOutBf16) hold[i + s][j & 7] = pack_bf16x2(x, y);
-          else {
-            hold[i + s][j & 7] = u;
-            hold1[kOut == kOutF32 ? i + s : 0][j & 7] = v;
+          for (int j = 0; j < kChunk; ++j) {
+            const int tok = kChunk * c + j;
+            if (tok >= t.m_valid) break;
+            const uint32_t at = smem_addr(base + G_::kOffStg) +
+                                ((rank * (kTok / splits) + tok / splits) * 2 * kFeat + q * 32 + lane) * 4;
+            const uint32_t to = pair::map_to(at, tok % splits);
+            pair::st_cluster_u32(to, p0[j]);
+            pair::st_cluster_u32(to + kFeat * 4, p1[j]);
           }
         }
-      }
-      tmem_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[acc]);
-      // ... then two chunks at a time are transposed through shared memory and leave row by
-      // row, four rows per warp.
+        break;  // a cluster has one tile
+      } else {
+        // First the accumulators move to registers (gated: through SwiGLU; bf16: both chains
+        // rounded into one register), so that the next tile's MMAs may overwrite them ...
+        uint32_t hold[kHold][kChunk], hold1[kOut == kOutF32 ? kHold : 1][kChunk];
+        uint32_t v0[2][kChunk], v1[2][kChunk];
 #pragma unroll
-      for (int i = 0; i < kHold; i += 2) {
-        if (2 * i + half >= n_chunks) break;
-        uint32_t* st = reinterpret_cast<uint32_t*>(stg + (kOut == kOutF32 ? 0 : buf * kStgBytes));
-        if (kOut == kOutF32) group_sync(half);  // both buffers are one, and free
+        for (int i = 0; i < kHold; i += 2) {  // two chunks at a time
+          if (2 * i + half >= n_chunks) break;
+          const uint32_t at = tb + kChunk * (2 * i + half);
+          tmem_ld8(at, v0[0]);
+          tmem_ld8(at + kTok, v1[0]);
+          if (i + 1 < kHold) {  // (columns past the tile's tokens hold what nothing reads)
+            tmem_ld8(at + 2 * kChunk, v0[1]);
+            tmem_ld8(at + 2 * kChunk + kTok, v1[1]);
+          }
+          tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 2 * kChunk; ++j) {
-          const int ii = i + (j >= kChunk ? 1 : 0);
-          if (ii >= kHold) break;
-          const uint32_t v = hold[ii][j & 7];  // gated: feature 32 q + lane; else two features
-          if (kOut != kOutF32) st[j * kFeat + q * 32 + lane] = v;
-          else
-            reinterpret_cast<uint2*>(st)[j * kFeat + q * 32 + lane] =
-                make_uint2(v, hold1[kOut == kOutF32 ? ii : 0][j & 7]);
-        }
-        group_sync(half);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int j = 4 * w4 + r;
-          const int tok = kChunk * (2 * (i + (j >= kChunk ? 1 : 0)) + half) + (j & (kChunk - 1));
-          if (tok >= t.m_valid) break;
-          const int64_t row = t.row0 + tok;
-          if (kGated) {
-            const float4 m = reinterpret_cast<const float4*>(st)[j * (kFeat / 4) + lane];
-            const uint32_t mx = __reduce_max_sync(0xffffffffu, max(max(abs_bits(m.x), abs_bits(m.y)),
-                                                                   max(abs_bits(m.z), abs_bits(m.w))));
-            const uint32_t s = q8_scale_byte(mx);
-            const float k = q8_inv_scale(s);
-            const int f = n0 + 4 * lane;
-            if (f < a.N)
-              *reinterpret_cast<uint32_t*>(a.q_out + row * a.N + f) =
-                  s == 255u ? 0x7F7F7F7Fu : q8_pack4(m.x * k, m.y * k, m.z * k, m.w * k);
-            if (lane == 0) a.q_scales[row * So + t.n_blk] = static_cast<uint8_t>(s);
-            if (t.n_blk == nbo - 1 && lane < So - nbo) a.q_scales[row * So + nbo + lane] = kQ8PadScale;
-          } else if (kOut == kOutBf16) {
-            const uint4 o = reinterpret_cast<const uint4*>(st)[j * (2 * kFeat / 8) + lane];
-            const int f = n0 + 8 * lane;
-            if (f < a.N) *reinterpret_cast<uint4*>(a.out + row * a.N + f) = o;
-          } else {
-#pragma unroll
-            for (int ch = 0; ch < 2; ++ch) {
-              float4 o = reinterpret_cast<const float4*>(st)[j * (2 * kFeat / 4) + ch * 32 + lane];
-              const int f = n0 + ch * kFeat + 4 * lane;
-              if (f < a.N) {
-                const int64_t at = row * a.N + f;
-                if (a.add_bf16) {
-                  const uint2 x = *reinterpret_cast<const uint2*>(a.add_bf16 + at);
-                  const float2 x0 = unpack_bf16x2(x.x), x1 = unpack_bf16x2(x.y);
-                  o.x += x0.x, o.y += x0.y, o.z += x1.x, o.w += x1.y;
-                } else {
-                  const float4 x = *reinterpret_cast<const float4*>(a.out_f32 + at);
-                  o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
-                }
-                *reinterpret_cast<float4*>(a.out_f32 + at) = o;
-              }
+          for (int j = 0; j < 2 * kChunk; ++j) {
+            const int s = j >= kChunk ? 1 : 0;
+            if (i + s >= kHold) break;
+            const uint32_t u = v0[s][j & 7], v = v1[s][j & 7];
+            const float x = __uint_as_float(u), y = __uint_as_float(v);
+            if (kGated) hold[i + s][j & 7] = __float_as_uint(swiglu(x, y));
+            else if (kOut == kOutBf16) hold[i + s][j & 7] = pack_bf16x2(x, y);
+            else {
+              hold[i + s][j & 7] = u;
+              hold1[kOut == kOutF32 ? i + s : 0][j & 7] = v;
             }
           }
         }
-        if (kOut != kOutF32) buf ^= 1u;
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[acc]);
+        // ... then two chunks at a time are transposed through shared memory and leave row by
+        // row, four rows per warp.
+#pragma unroll
+        for (int i = 0; i < kHold; i += 2) {
+          if (2 * i + half >= n_chunks) break;
+          uint32_t* st = reinterpret_cast<uint32_t*>(stg + (kOut == kOutF32 ? 0 : buf * kStgBytes));
+          if (kOut == kOutF32) group_sync(half);  // both buffers are one, and free
+#pragma unroll
+          for (int j = 0; j < 2 * kChunk; ++j) {
+            const int ii = i + (j >= kChunk ? 1 : 0);
+            if (ii >= kHold) break;
+            const uint32_t v = hold[ii][j & 7];  // gated: feature 32 q + lane; else two features
+            if (kOut != kOutF32) st[j * kFeat + q * 32 + lane] = v;
+            else
+              reinterpret_cast<uint2*>(st)[j * kFeat + q * 32 + lane] =
+                  make_uint2(v, hold1[kOut == kOutF32 ? ii : 0][j & 7]);
+          }
+          group_sync(half);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int j = 4 * w4 + r;
+            const int tok = kChunk * (2 * (i + (j >= kChunk ? 1 : 0)) + half) + (j & (kChunk - 1));
+            if (tok >= t.m_valid) break;
+            const int64_t row = t.row0 + tok;
+            if (kGated) {
+              store_gated_row(a, row, t.n_blk, lane, reinterpret_cast<const float4*>(st)[j * (kFeat / 4) + lane]);
+            } else if (kOut == kOutBf16) {
+              const uint4 o = reinterpret_cast<const uint4*>(st)[j * (2 * kFeat / 8) + lane];
+              const int f = n0 + 8 * lane;
+              if (f < a.N) *reinterpret_cast<uint4*>(a.out + row * a.N + f) = o;
+            } else {
+#pragma unroll
+              for (int ch = 0; ch < 2; ++ch) {
+                const int f = n0 + ch * kFeat + 4 * lane;
+                if (f < a.N)
+                  add_f32(a, row * a.N + f, reinterpret_cast<const float4*>(st)[j * (2 * kFeat / 4) + ch * 32 + lane]);
+              }
+            }
+          }
+          if (kOut != kOutF32) buf ^= 1u;
+        }
       }
     }
   }
@@ -575,9 +628,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
           if (!mbar_wait_bounded(&full[s], (issued_parity >> s) & 1u, drain_wait_limit(a.wait_limit_ns), never_flag))
             atomicOr(a.status, kStatusTimeoutDrain);
     }
-    if (warp == 1 && lane == 0) {
-      mma_commit(drain);
-      if (!mbar_wait_bounded(drain, 0, drain_wait_limit(a.wait_limit_ns), never_flag))
+    if (warp == 1) {  // by the lane that issued them: the same one is elected every time
+      if (elect_one()) mma_commit(drain);
+      __syncwarp();
+      if (!mbar_wait_converged(drain, 0, drain_wait_limit(a.wait_limit_ns), never_flag) && lane == 0)
         atomicOr(a.status, kStatusTimeoutDrain);
     }
   }
@@ -587,24 +641,74 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
     tc_fence_after();
     tmem_dealloc(tmem_base, kTmemCols);
   }
+  if (kSplit) {
+    __syncwarp();
+    pair::cluster_sync();  // the partial sums have arrived
+    if (tile0 >= total || warp < 2 || warp >= 2 + kEpiWarps) return;
+    const Q8Tile t = decode_tile<kTok>(a, tile_start, tile0);
+    const int slots = kTok / splits;
+    for (int slot = warp - 2; slot * splits + rank < t.m_valid; slot += kEpiWarps) {
+      float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
+      for (int s = 0; s < splits; ++s) {  // in the order of K
+        const float4* p = reinterpret_cast<const float4*>(base + G_::kOffStg) + (s * slots + slot) * (kFeat / 2) + lane;
+        const float4 x = p[0], y = p[kFeat / 4];
+        g.x += x.x, g.y += x.y, g.z += x.z, g.w += x.w;
+        u.x += y.x, u.y += y.y, u.z += y.z, u.w += y.w;
+      }
+      const int64_t row = t.row0 + slot * splits + rank;
+      const int n0 = t.n_blk * kTileFeat;
+      if (kGated) {
+        store_gated_row(a, row, t.n_blk, lane, make_float4(swiglu(g.x, u.x), swiglu(g.y, u.y), swiglu(g.z, u.z),
+                                                           swiglu(g.w, u.w)));
+      } else if (n0 + 8 * lane < a.N) {
+        const int64_t at = row * a.N + n0 + 8 * lane;
+        if (kOut == kOutBf16) {
+          *reinterpret_cast<uint4*>(a.out + at) = make_uint4(pack_bf16x2(g.x, u.x), pack_bf16x2(g.y, u.y),
+                                                             pack_bf16x2(g.z, u.z), pack_bf16x2(g.w, u.w));
+        } else {
+          add_f32(a, at, make_float4(g.x, u.x, g.y, u.y));
+          add_f32(a, at + 4, make_float4(g.z, u.z, g.w, u.w));
+        }
+      }
+    }
+  }
 }
 
-template <int kOut, int kTok>
+template <int kOut, int kTok, bool kSplit>
 cudaError_t launch_one(const Q8GemmArgs& a, int grid, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(gemm_q8_kernel<kOut, kTok>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(gemm_q8_kernel<kOut, kTok, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(Geo<kTok>::kSmemBytes));
   if (e != cudaSuccess) return e;
-  gemm_q8_kernel<kOut, kTok><<<grid, kThreads, Geo<kTok>::kSmemBytes, s>>>(a);
-  return cudaGetLastError();
+  if (!kSplit) {
+    gemm_q8_kernel<kOut, kTok, kSplit><<<grid, kThreads, Geo<kTok>::kSmemBytes, s>>>(a);
+    return cudaGetLastError();
+  }
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = a.splits;
+  cluster.val.clusterDim.y = 1;
+  cluster.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Geo<kTok>::kSmemBytes;
+  cfg.stream = s;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gemm_q8_kernel<kOut, kTok, kSplit>, a);
 }
 
 template <int kOut>
 cudaError_t launch_tok(const Q8GemmArgs& a, int tok, int grid, cudaStream_t s) {
-  if (tok == 32) return launch_one<kOut, 32>(a, grid, s);
+  if (a.splits > 1) return launch_one<kOut, 32, true>(a, grid, s);
+  if (tok == 32) return launch_one<kOut, 32, false>(a, grid, s);
   if constexpr (kOut != kOutF32)
-    if (tok == 240) return launch_one<kOut, 240>(a, grid, s);
-  return launch_one<kOut, 112>(a, grid, s);
+    if (tok == 240) return launch_one<kOut, 240, false>(a, grid, s);
+  return launch_one<kOut, 112, false>(a, grid, s);
 }
+
+// Tiles of `tok` rows that R rows in E groups make at most.
+int64_t token_tiles(int64_t R, int E, int tok) { return (R + (tok - 1) * std::min<int64_t>(E, R)) / tok; }
 }  // namespace
 
 // Token tile by rows per group g = R / E, measured over K = 256 .. 7168 on 32 groups (us, plain
@@ -629,11 +733,26 @@ int q8_token_tile(int64_t R, int E, int N, int K, bool gated, int num_sms) {
   return large ? 240 : 112;
 }
 
-cudaError_t launch_gemm_q8(const Q8GemmArgs& a, int tok, int num_sms, cudaStream_t s) {
+// CTAs that share a 32-token tile along K: the most of 8, 4, 2 whose clusters run side by side
+// (of 148 SMs, 15 clusters of 8 CTAs, 33 of 4, 74 of 2) and that leave each CTA a group of
+// four K blocks. One row, N = 128, K = 7168, gated: 28.4 us alone, 18.7, 14.0 and 10.5 with
+// 2, 4 and 8; 16 tiles: 28.9, 18.7, 14.6 and 18.8 (the 16th cluster of 8 runs afterwards).
+static int q8_splits(int64_t tiles, int K, int num_sms) {
+  const int groups = (K + 511) / 512;
+  for (int s = 8; s > 1; s >>= 1) {
+    const int idle = s == 8 ? 28 : s == 4 ? 16 : 0;
+    if (tiles * s <= num_sms - idle && groups >= s) return s;
+  }
+  return 1;
+}
+
+cudaError_t launch_gemm_q8(const Q8GemmArgs& args, int tok, int num_sms, cudaStream_t s) {
+  Q8GemmArgs a = args;
   const bool gated = a.q_out != nullptr;
   const int64_t n_tiles = (a.N + (gated ? 127 : 255)) / (gated ? 128 : 256);
-  const int64_t bound = ((a.R + tok - 1) / tok + a.E) * n_tiles;
-  const int grid = static_cast<int>(bound < num_sms ? bound : num_sms);
+  const int64_t bound = token_tiles(a.R, a.E, tok) * n_tiles;
+  a.splits = tok == 32 ? q8_splits(bound, a.K, num_sms) : 1;
+  const int grid = static_cast<int>(a.splits > 1 ? bound * a.splits : std::min<int64_t>(bound, num_sms));
   if (gated) return launch_tok<kOutGated>(a, tok, grid, s);
   return a.out_f32 ? launch_tok<kOutF32>(a, tok, grid, s) : launch_tok<kOutBf16>(a, tok, grid, s);
 }

@@ -362,6 +362,7 @@ struct Q8GemmArgs {
   uint8_t* q_scales;         // [R, q8_scale_cols(N)]
   float* out_f32;            // [R, N]
   const bf16* add_bf16;      // [R, N] or nullptr
+  int splits;                // set by launch_gemm_q8: CTAs that share a tile along K
   uint32_t* status;
   uint64_t wait_limit_ns;
 };

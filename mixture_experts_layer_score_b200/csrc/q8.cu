@@ -72,9 +72,9 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const bf16* __restri
 
 // One block of threads per 128 x 128 tile of one expert's matrix; the tile stays in registers
 // between the maximum and the encoding (thread: eight columns of rows i, i + 16, ...).
-__global__ void __launch_bounds__(256, 4) quantize_weights_kernel(const bf16* __restrict__ W, int64_t tiles, int N, int K,
-                                                               uint8_t* __restrict__ q,
-                                                               uint8_t* __restrict__ scales) {
+__global__ void __launch_bounds__(256, 4) quantize_weights_kernel(const bf16* __restrict__ W, int64_t tiles, int N,
+                                                                  int K, uint8_t* __restrict__ q,
+                                                                  uint8_t* __restrict__ scales) {
   __shared__ uint32_t s_max[8];
   const int nkb = (K + kQ8Block - 1) / kQ8Block, nnb = (N + kQ8Block - 1) / kQ8Block, S = q8_scale_cols(K);
   const int col = (threadIdx.x & 15) * 8, row = threadIdx.x >> 4;
@@ -91,7 +91,8 @@ __global__ void __launch_bounds__(256, 4) quantize_weights_kernel(const bf16* __
     for (int i = 0; i < 8; ++i) {
       const int n = row + 16 * i;
       v[i] = make_uint4(0, 0, 0, 0);
-      if (k < K && nb * kQ8Block + n < N) v[i] = *reinterpret_cast<const uint4*>(W + base + static_cast<int64_t>(n) * K);
+      if (k < K && nb * kQ8Block + n < N)
+        v[i] = *reinterpret_cast<const uint4*>(W + base + static_cast<int64_t>(n) * K);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {

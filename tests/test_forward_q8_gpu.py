@@ -78,8 +78,8 @@ def test_layer(name, T):
     assert near(NP(out["h"])[rows], reference(layer, u, NP(gpu["x"]), idx, gates, cfg.n_shared, rows))
     # the 8-bit operands themselves: three roundings of at most 2^-4 in each expert term
     part = NP(o16["h"]) - NP(gpu["x"])
-    assert np.linalg.norm(NP(out["h"]) - NP(o16["h"])) <= 3 * 2.0 ** -4 * np.linalg.norm(part) + 2.0 ** -8 * np.linalg.norm(
-        NP(o16["h"]))
+    off = np.linalg.norm(NP(out["h"]) - NP(o16["h"]))
+    assert off <= 3 * 2.0 ** -4 * np.linalg.norm(part) + 2.0 ** -8 * np.linalg.norm(NP(o16["h"]))
     # rows that the caller has quantised, and a base that is not x
     x_q = layer.alloc_rows(T)
     M.dsmoe_q8_quantize(layer.handle, T, cfg.d_model, gpu["x"], *x_q)

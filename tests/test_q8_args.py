@@ -59,11 +59,13 @@ class TestHandle:
     def test_quantize_sizes(self, R, C, expect):
         assert self.status(lambda: M.dsmoe_q8_quantize(self.h, R, C, 16, 16, 16, 0)) == expect
 
-    @pytest.mark.parametrize("x,q,s", [(None, 16, 16), (16, None, 16), (16, 16, None), (8, 16, 16), (16, 24, 16), (16, 16, 4)])
+    @pytest.mark.parametrize("x,q,s", [(None, 16, 16), (16, None, 16), (16, 16, None), (8, 16, 16), (16, 24, 16),
+                                       (16, 16, 4)])
     def test_quantize_pointers(self, x, q, s):
         assert self.status(lambda: M.dsmoe_q8_quantize(self.h, 1, 16, x, q, s, 0)) == 1
 
-    @pytest.mark.parametrize("E,N,K,expect", [(0, 1, 16, 1), (1, 0, 16, 1), (513, 1, 16, 2), (1, 32769, 16, 2), (1, 1, 8, 2)])
+    @pytest.mark.parametrize("E,N,K,expect", [(0, 1, 16, 1), (1, 0, 16, 1), (513, 1, 16, 2), (1, 32769, 16, 2),
+                                              (1, 1, 8, 2)])
     def test_quantize_weights_sizes(self, E, N, K, expect):
         assert self.status(lambda: M.dsmoe_q8_quantize_weights(self.h, E, N, K, 16, 16, 16, 0)) == expect
 
@@ -85,8 +87,9 @@ class TestHandle:
             assert self.status(lambda: M.dsmoe_norm_backward(self.h, a["T"], a["dy"], a["dres"], a["r"], a["w"],
                                                              a["eps"], a["dx"], a["dw"], 0)) == expect, bad
 
-    @pytest.mark.parametrize("E,R,N,K,expect", [(0, 1, 8, 16, 1), (1, -1, 8, 16, 1), (1, 1, 0, 16, 1), (1, 1, 12, 16, 2),
-                                                (1, 1, 8, 8, 2), (1, 1, 32776, 16, 2), (1, 1, 8, 32784, 2),
+    @pytest.mark.parametrize("E,R,N,K,expect", [(0, 1, 8, 16, 1), (1, -1, 8, 16, 1), (1, 1, 0, 16, 1),
+                                                (1, 1, 12, 16, 2), (1, 1, 8, 8, 2), (1, 1, 32776, 16, 2),
+                                                (1, 1, 8, 32784, 2),
                                                 (513, 1, 8, 16, 2), (1, 1 << 31, 8, 16, 2)])
     def test_product_sizes(self, E, R, N, K, expect):
         p = [16] * 6

@@ -48,7 +48,8 @@ def q8_weights(W):
 
 
 # ------------------------------------------------------------------------- quantisation
-@pytest.mark.parametrize("R,C", [(1, 16), (1, 128), (3, 144), (33, 704), (512, 256), (130, 1280), (7, 7168), (2, 32768)])
+@pytest.mark.parametrize("R,C", [(1, 16), (1, 128), (3, 144), (33, 704), (512, 256), (130, 1280), (7, 7168),
+                                 (2, 32768)])
 def test_quantize_rows(handle, R, C):
     x = rows(R, C, seed=R + C, spread=8.0)
     if R > 2:
@@ -162,6 +163,11 @@ PRODUCTS = [  # counts of each expert, first row, rows behind the last, N, K
     ([511, 240, 241, 16], 0, 0, 256, 528),
     ([300, 20], 0, 0, 512, 1296),
     ([600], 1, 0, 2304, 256),
+    # few tiles: the CTAs of a cluster share one along K (8, 4 and 2 of them, uneven ranges)
+    ([5], 0, 0, 1024, 7168),
+    ([1], 1, 1, 776, 4624),
+    ([32], 0, 0, 2048, 2064),
+    ([0, 40, 3], 0, 2, 520, 1552),
 ]
 
 
@@ -326,4 +332,28 @@ def test_norm_then_gated_then_product_on_a_stream_and_in_a_graph():
     assert torch.equal(eager, y) and float(y.float().abs().sum()) > 0
     assert M.dsmoe_get_status(h) == M.DSMOE_OK
     del graph
+    M.dsmoe_destroy(h)
+
+
+@pytest.mark.parametrize("counts,N,K", [([300, 41, 7], 256, 1024), ([3], 256, 7168)])  # persistent; a cluster per tile
+def test_wait_limit_runs_out_then_the_handle_recovers(counts, N, K):
+    """With a limit of 1 ns some role gives up, the kernel drains what it started and returns, the
+    status says so once; with the default limit the same handle's products are right again."""
+    h = M.dsmoe_create(M.make_cfg(d_model=64, n_routed=1, top_k=1, d_ff=64, max_tokens=1))
+    M.dsmoe_set_wait_limit(h, 1)
+    E, R = len(counts), sum(counts)
+    q = torch.zeros(R, K, dtype=torch.uint8, device="cuda")
+    s = torch.full((R, M.dsmoe_q8_scale_cols(K)), 127, dtype=torch.uint8, device="cuda")
+    W = torch.zeros(E, N, K, dtype=torch.uint8, device="cuda")
+    ws = torch.full((E, N // 128, M.dsmoe_q8_scale_cols(K)), 127, dtype=torch.uint8, device="cuda")
+    out = torch.empty(R, N, dtype=torch.bfloat16, device="cuda")
+    M.dsmoe_q8_matmul(h, E, R, N, K, offsets_of(counts), q, s, W, ws, out)
+    M.dsmoe_q8_gated_matmul(h, E, R, N, K, offsets_of(counts), q, s, W, ws, W, ws, *q8_empty(R, N))
+    torch.cuda.synchronize()
+    assert M.dsmoe_get_status(h) == M.DSMOE_ERR_DEVICE_TIMEOUT
+    assert M.dsmoe_get_status(h) == M.DSMOE_OK
+    M.dsmoe_set_wait_limit(h, 2_000_000_000)
+    check_product(h, counts, 0, 0, N, K)
+    check_gated(h, counts, 0, 0, N, K)
+    assert M.dsmoe_get_status(h) == M.DSMOE_OK
     M.dsmoe_destroy(h)
