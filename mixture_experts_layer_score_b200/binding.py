@@ -673,11 +673,12 @@ class DSMoEQ8(DSMoE):
 
     def forward(self, x, token_ids=None, out=None, with_scores: bool = False, stream=None, residual=None, x_q=None):
         """The layer on x; x_q: its 8-bit rows (values, scales) where the caller has them (else they
-        are made here); residual: what the layer's output is added to in place of x."""
+        are made here and returned as "x_q", so that they live as long as the outputs, whatever
+        the stream); residual: what the layer's output is added to in place of x."""
         T = x.shape[0]
         o = self.alloc_outputs(T, with_scores) if out is None else out
         if x_q is None:
-            x_q = self.alloc_rows(T)
+            x_q = o["x_q"] = self.alloc_rows(T)
             dsmoe_q8_quantize(self.handle, T, self.cfg.d_model, x, *x_q, stream)
         w = self.w
         dsmoe_forward_q8(self.handle, T, x, *x_q, residual, token_ids, w.get("W_router"), w.get("b"), self._weights,
@@ -687,11 +688,11 @@ class DSMoEQ8(DSMoE):
 
     def forward_norm(self, x, residual, w, eps: float, token_ids=None, with_scores: bool = False, stream=None):
         """A block: r = x + residual, u = RMSNorm(r) w, h = r + the layer's experts on u. Returns the
-        layer's outputs and "r", "u"."""
+        layer's outputs and "r", "u", "x_q" (the 8-bit rows of u)."""
         import torch
         T = x.shape[0]
         r, u, x_q = torch.empty_like(x), torch.empty_like(x), self.alloc_rows(T)
         dsmoe_norm_q8(self.handle, T, x, residual, w, eps, r, u, *x_q, stream)
         o = self.forward(u, token_ids, None, with_scores, stream, r, x_q)
-        o["r"], o["u"] = r, u
+        o["r"], o["u"], o["x_q"] = r, u, x_q
         return o

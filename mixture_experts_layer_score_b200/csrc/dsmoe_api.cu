@@ -1947,7 +1947,7 @@ DSMOE_EXPORT dsmoe_status dsmoe_q8_quantize(dsmoe_handle* h, int64_t R, int32_t 
   DeviceGuard g(h->device);
   if (!g.ok) return fail(DSMOE_ERR_CUDA, "cannot select device %d", h->device);
   CUDA_TRY(dsmoe::launch_quantize_rows(static_cast<const bf16*>(x), R, C, static_cast<uint8_t*>(q),
-                                       static_cast<uint8_t*>(scales), h->num_sms, static_cast<cudaStream_t>(stream)));
+                                       static_cast<uint8_t*>(scales), static_cast<cudaStream_t>(stream)));
   h->launches += 1;
   return DSMOE_OK;
 }
@@ -1960,8 +1960,7 @@ DSMOE_EXPORT dsmoe_status dsmoe_q8_quantize_weights(dsmoe_handle* h, int32_t E, 
   DeviceGuard g(h->device);
   if (!g.ok) return fail(DSMOE_ERR_CUDA, "cannot select device %d", h->device);
   CUDA_TRY(dsmoe::launch_quantize_weights(static_cast<const bf16*>(W), E, N, K, static_cast<uint8_t*>(q),
-                                          static_cast<uint8_t*>(scales), h->num_sms,
-                                          static_cast<cudaStream_t>(stream)));
+                                          static_cast<uint8_t*>(scales), static_cast<cudaStream_t>(stream)));
   h->launches += 1;
   return DSMOE_OK;
 }

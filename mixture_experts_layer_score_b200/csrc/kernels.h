@@ -303,9 +303,8 @@ cudaError_t launch_gateup_pair(const GemmArgs& a, int clusters, cudaStream_t s);
 // ---------------------------------------------------------------- 8-bit path (q8.cu, q8.cuh)
 // q [R, C] e4m3 and scales [R, q8_scale_cols(C)] of the bf16 rows x (C a multiple of 16);
 // q [E, N, K] and scales [E, ceil(N / 128), q8_scale_cols(K)] of the weights W.
-cudaError_t launch_quantize_rows(const bf16* x, int64_t R, int C, uint8_t* q, uint8_t* scales, int num_sms,
-                                 cudaStream_t s);
-cudaError_t launch_quantize_weights(const bf16* W, int E, int N, int K, uint8_t* q, uint8_t* scales, int num_sms,
+cudaError_t launch_quantize_rows(const bf16* x, int64_t R, int C, uint8_t* q, uint8_t* scales, cudaStream_t s);
+cudaError_t launch_quantize_weights(const bf16* W, int E, int N, int K, uint8_t* q, uint8_t* scales,
                                     cudaStream_t s);
 
 // The 8-bit rows' permutation: as launch_permute_gather, for values [T, d] and scales

@@ -44,29 +44,37 @@ __device__ __forceinline__ uint32_t half_warp_max(uint32_t v) {
   return v;
 }
 
-// Sixteen lanes hold one block of 128 values, eight each.
-__global__ void __launch_bounds__(256) quantize_rows_kernel(const bf16* __restrict__ x, int64_t R, int C,
+// Sixteen lanes hold one block of 128 values, eight each; every thread has kQuantUnits blocks in
+// flight.
+constexpr int kQuantUnits = 4;
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const bf16* __restrict__ x, uint32_t units, int C,
                                                             uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
-  const int nb = (C + kQ8Block - 1) / kQ8Block, S = q8_scale_cols(C);
-  const int64_t units = R * nb, step = static_cast<int64_t>(gridDim.x) * 16;
-  const int sub = threadIdx.x & 15;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
-  // every lane of a warp runs the same number of rounds (the shuffles need them all)
-  const int64_t warp_first = static_cast<int64_t>(blockIdx.x) * 16 + ((threadIdx.x >> 5) << 1);
-  for (int64_t u0 = warp_first, u = first; u0 < units; u0 += step, u += step) {
-    const bool row_ok = u < units;
-    const int64_t r = row_ok ? u / nb : 0;
-    const int b = row_ok ? static_cast<int>(u - r * nb) : 0;
-    const int c = b * kQ8Block + sub * 8;
-    const bool ok = row_ok && c < C;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (ok) v = *reinterpret_cast<const uint4*>(x + r * C + c);
+  const int nb = (C + kQ8Block - 1) / kQ8Block, S = q8_scale_cols(C), sub = threadIdx.x & 15;
+  const uint32_t first = blockIdx.x * (16u * kQuantUnits) + (threadIdx.x >> 4);
+  uint4 v[kQuantUnits];
+  uint32_t row[kQuantUnits];
+  int blk[kQuantUnits];
+#pragma unroll
+  for (int i = 0; i < kQuantUnits; ++i) {
+    const uint32_t u = first + 16u * i;
+    row[i] = u / static_cast<uint32_t>(nb);
+    blk[i] = static_cast<int>(u - row[i] * nb);
+    const int c = blk[i] * kQ8Block + sub * 8;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (u < units && c < C) v[i] = *reinterpret_cast<const uint4*>(x + static_cast<int64_t>(row[i]) * C + c);
+  }
+#pragma unroll
+  for (int i = 0; i < kQuantUnits; ++i) {
+    const bool ok = first + 16u * i < units;
+    const int c = blk[i] * kQ8Block + sub * 8;
+    const int64_t r = row[i];
     float f[8];
-    unpack8(v, f);
+    unpack8(v[i], f);
     const uint32_t s = q8_scale_byte(half_warp_max(amax8(f)));
-    if (ok) *reinterpret_cast<uint2*>(q + r * C + c) = encode8(f, s);
-    if (row_ok && sub == 0) scales[r * S + b] = static_cast<uint8_t>(s);
-    if (row_ok && b == nb - 1 && sub < S - nb) scales[r * S + nb + sub] = kQ8PadScale;
+    if (!ok) continue;
+    if (c < C) *reinterpret_cast<uint2*>(q + r * C + c) = encode8(f, s);
+    if (sub == 0) scales[r * S + blk[i]] = static_cast<uint8_t>(s);
+    if (blk[i] == nb - 1 && sub < S - nb) scales[r * S + nb + sub] = kQ8PadScale;
   }
 }
 
@@ -454,20 +462,18 @@ int norm_threads(int d) {
 
 }  // namespace
 
-cudaError_t launch_quantize_rows(const bf16* x, int64_t R, int C, uint8_t* q, uint8_t* scales, int num_sms,
-                                 cudaStream_t s) {
+cudaError_t launch_quantize_rows(const bf16* x, int64_t R, int C, uint8_t* q, uint8_t* scales, cudaStream_t s) {
   const int64_t units = R * ((C + kQ8Block - 1) / kQ8Block);
-  int64_t grid = (units + 15) / 16;
-  if (grid > 8 * num_sms) grid = 8 * num_sms;
-  if (grid < 1) return cudaSuccess;
-  quantize_rows_kernel<<<static_cast<int>(grid), 256, 0, s>>>(x, R, C, q, scales);
+  if (units == 0) return cudaSuccess;
+  if (units > INT32_MAX - 64) return cudaErrorInvalidValue;  // more values than any GPU's memory holds
+  const int grid = static_cast<int>((units + 16 * kQuantUnits - 1) / (16 * kQuantUnits));
+  quantize_rows_kernel<<<grid, 256, 0, s>>>(x, static_cast<uint32_t>(units), C, q, scales);
   return cudaGetLastError();
 }
 
-cudaError_t launch_quantize_weights(const bf16* W, int E, int N, int K, uint8_t* q, uint8_t* scales, int num_sms,
+cudaError_t launch_quantize_weights(const bf16* W, int E, int N, int K, uint8_t* q, uint8_t* scales,
                                     cudaStream_t s) {
   const int64_t tiles = static_cast<int64_t>(E) * ((N + kQ8Block - 1) / kQ8Block) * ((K + kQ8Block - 1) / kQ8Block);
-  (void)num_sms;
   // a block per tile: the blocks' phases drift apart and keep the memory busy (32 x 2048 x 7168
   // weights: 223 us, 6.3 TB/s, against 242 with as many blocks as are resident at once)
   const int64_t grid = std::min<int64_t>(tiles, 1 << 30);
