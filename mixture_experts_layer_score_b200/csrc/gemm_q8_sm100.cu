@@ -213,18 +213,31 @@ __device__ __forceinline__ float swiglu(float g, float u) {
   return g * r * u;
 }
 
-// The warp stores one row's block of 128 gated outputs in 8 bits, four features per lane, and
-// its scale (the last block of a row also the row's padding scales).
-__device__ __forceinline__ void store_gated_row(const Q8GemmArgs& a, int64_t row, int blk, int lane, const float4& m) {
+// The warp stores a block of 128 gated outputs in 8 bits for the first n of kRows rows in a row,
+// four features per lane, and their scales (the last block of a row also the row's padding
+// scales). The rows are worked on side by side: their maxima are reduced back to back.
+template <int kRows>
+__device__ __forceinline__ void store_gated_rows(const Q8GemmArgs& a, int64_t row, int n, int blk, int lane,
+                                                 const float4 (&m)[kRows]) {
   const int So = q8_scale_cols(a.N), nb = (a.N + kFeat - 1) / kFeat, f = blk * kFeat + 4 * lane;
-  const uint32_t s = q8_scale_byte(__reduce_max_sync(
-      0xffffffffu, max(max(abs_bits(m.x), abs_bits(m.y)), max(abs_bits(m.z), abs_bits(m.w)))));
-  const float k = q8_inv_scale(s);
-  if (f < a.N)
-    *reinterpret_cast<uint32_t*>(a.q_out + row * a.N + f) =
-        s == 255u ? 0x7F7F7F7Fu : q8_pack4(m.x * k, m.y * k, m.z * k, m.w * k);
-  if (lane == 0) a.q_scales[row * So + blk] = static_cast<uint8_t>(s);
-  if (blk == nb - 1 && lane < So - nb) a.q_scales[row * So + nb + lane] = kQ8PadScale;
+  uint32_t s[kRows], mine = 0;
+#pragma unroll
+  for (int r = 0; r < kRows; ++r)
+    s[r] = __reduce_max_sync(0xffffffffu, max(max(abs_bits(m[r].x), abs_bits(m[r].y)),
+                                              max(abs_bits(m[r].z), abs_bits(m[r].w))));
+  uint8_t* q = a.q_out + row * a.N + f;
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    s[r] = q8_scale_byte(s[r]);
+    if (lane == r) mine = s[r];
+    const float k = q8_inv_scale(s[r]);
+    const uint32_t v = s[r] == 255u ? 0x7F7F7F7Fu : q8_pack4(m[r].x * k, m[r].y * k, m[r].z * k, m[r].w * k);
+    if (r < n && f < a.N) *reinterpret_cast<uint32_t*>(q + static_cast<int64_t>(r) * a.N) = v;
+  }
+  uint8_t* scales = a.q_scales + row * So;
+  if (lane < n) scales[lane * So + blk] = static_cast<uint8_t>(mine);
+  if (blk == nb - 1 && lane < So - nb)
+    for (int r = 0; r < n; ++r) scales[r * So + nb + lane] = kQ8PadScale;
 }
 
 // Four fp32 outputs at `at`: added to the bf16 rows given, or to what is there.
@@ -600,26 +613,34 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
                   make_uint2(v, hold1[kOut == kOutF32 ? ii : 0][j & 7]);
           }
           group_sync(half);
+          // this warp's four rows of the sixteen, neighbours in the output
+          const int j0 = 4 * w4, tok = kChunk * (2 * (i + (j0 >= kChunk ? 1 : 0)) + half) + (j0 & (kChunk - 1));
+          const int n_rows = t.m_valid - tok;
+          const int64_t row = t.row0 + tok;
+          if (kGated) {
+            float4 m[4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int j = 4 * w4 + r;
-            const int tok = kChunk * (2 * (i + (j >= kChunk ? 1 : 0)) + half) + (j & (kChunk - 1));
-            if (tok >= t.m_valid) break;
-            const int64_t row = t.row0 + tok;
-            if (kGated) {
-              store_gated_row(a, row, t.n_blk, lane, reinterpret_cast<const float4*>(st)[j * (kFeat / 4) + lane]);
-            } else if (kOut == kOutBf16) {
-              const uint4 o = reinterpret_cast<const uint4*>(st)[j * (2 * kFeat / 8) + lane];
-              const int f = n0 + 8 * lane;
-              if (f < a.N) *reinterpret_cast<uint4*>(a.out + row * a.N + f) = o;
-            } else {
+            for (int r = 0; r < 4; ++r) m[r] = reinterpret_cast<const float4*>(st)[(j0 + r) * (kFeat / 4) + lane];
+            if (n_rows > 0) store_gated_rows<4>(a, row, min(n_rows, 4), t.n_blk, lane, m);
+          } else if (kOut == kOutBf16) {
+            const int f = n0 + 8 * lane;
+            uint4 o[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[r] = reinterpret_cast<const uint4*>(st)[(j0 + r) * (2 * kFeat / 8) + lane];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (r < n_rows && f < a.N)
+                *reinterpret_cast<uint4*>(a.out + row * a.N + f + static_cast<int64_t>(r) * a.N) = o[r];
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
               for (int ch = 0; ch < 2; ++ch) {
                 const int f = n0 + ch * kFeat + 4 * lane;
-                if (f < a.N)
-                  add_f32(a, row * a.N + f, reinterpret_cast<const float4*>(st)[j * (2 * kFeat / 4) + ch * 32 + lane]);
+                if (r < n_rows && f < a.N)
+                  add_f32(a, (row + r) * a.N + f,
+                          reinterpret_cast<const float4*>(st)[(j0 + r) * (2 * kFeat / 4) + ch * 32 + lane]);
               }
-            }
           }
           if (kOut != kOutF32) buf ^= 1u;
         }
@@ -666,8 +687,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
       const int64_t row = t.row0 + slot * splits + rank;
       const int n0 = t.n_blk * kTileFeat;
       if (kGated) {
-        store_gated_row(a, row, t.n_blk, lane, make_float4(swiglu(g.x, u.x), swiglu(g.y, u.y), swiglu(g.z, u.z),
-                                                           swiglu(g.w, u.w)));
+        const float4 m[1] = {
+            make_float4(swiglu(g.x, u.x), swiglu(g.y, u.y), swiglu(g.z, u.z), swiglu(g.w, u.w))};
+        store_gated_rows<1>(a, row, 1, t.n_blk, lane, m);
       } else if (n0 + 8 * lane < a.N) {
         const int64_t at = row * a.N + n0 + 8 * lane;
         if (kOut == kOutBf16) {
