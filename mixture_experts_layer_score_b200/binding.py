@@ -410,40 +410,40 @@ def dsmoe_bias_update(handle, T, counts, alpha, b, stream=None):
 # ---- the 8-bit path. Byte tensors (e4m3 values, e8m0 scales) may be of any one-byte dtype, e.g.
 # torch.float8_e4m3fn and torch.float8_e8m0fnu.
 _DTYPES: Dict[str, tuple] = {}
+_raw_stream = None
 
 
-def _dtypes(kind: str) -> tuple:
-    if not _DTYPES:
-        import torch
-        _DTYPES.update(bf16=(torch.bfloat16,), f32=(torch.float32,), i32=(torch.int32,),
-                       q8=(torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.uint8, torch.int8))
-    return _DTYPES[kind]
+def _setup():
+    import torch
+    global _raw_stream
+    _raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream() without the Stream object
+    _DTYPES.update(bf16=(torch.bfloat16,), f32=(torch.float32,), i32=(torch.int32,),
+                   q8=(torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.uint8, torch.int8))
 
 
 def _take(where: str, handle, stream, *tensors):
     """Check the torch tensors of a call ((name, tensor, kind, elements); raw addresses pass) and
     return their addresses in order, and the stream: the caller's, or the current stream of
     the handle's device."""
+    if not _DTYPES:
+        _setup()
     device = _handles[handle][0] if handle in _handles else None
-    kinds = _DTYPES or (_dtypes("bf16"), _DTYPES)[1]
     ptrs = []
     for name, t, kind, n in tensors:
-        if t is None or t.__class__ is int:
-            ptrs.append(t)
-            continue
-        if t.dtype not in kinds[kind] or t.numel() != n or not t.is_contiguous() or \
-                (t.get_device() != device if device is not None else not t.is_cuda):
-            _refuse(where, name, t, kind, n)
-        ptrs.append(t.data_ptr())
+        if t is not None and t.__class__ is not int:
+            if t.dtype not in _DTYPES[kind] or t.numel() != n or not t.is_contiguous() or \
+                    (t.get_device() != device if device is not None else not t.is_cuda):
+                _refuse(where, name, t, kind, n)
+            t = t.data_ptr()
+        ptrs.append(t)
     if stream is None and device is not None:
-        import torch
-        stream = torch._C._cuda_getCurrentRawStream(device)  # current_stream() without the Stream object
+        return ptrs, _raw_stream(device)
     return ptrs, _stream(stream)
 
 
 def _refuse(where: str, name: str, t, kind: str, n: int):
-    if t.dtype not in _dtypes(kind):
-        why = f"is {t.dtype}, not {' or '.join(map(str, _dtypes(kind)))}"
+    if t.dtype not in _DTYPES[kind]:
+        why = f"is {t.dtype}, not {' or '.join(map(str, _DTYPES[kind]))}"
     elif t.numel() != n:
         why = f"has {t.numel()} elements, not {n}"
     elif not t.is_contiguous():
@@ -455,10 +455,12 @@ def _refuse(where: str, name: str, t, kind: str, n: int):
 
 def _norm_width(where, handle, w) -> int:
     """d of the handle's rows, which w has to match."""
-    d = w.numel() if hasattr(w, "numel") else 0
-    if handle in _handles and hasattr(w, "numel") and d != _handles[handle][1]:
-        raise DsmoeError(DSMOE_ERR_INVALID_ARG, where, f"w has {d} elements, not d_model = {_handles[handle][1]}")
-    return _handles[handle][1] if handle in _handles else d
+    known = _handles.get(handle)
+    if known is None:
+        return w.numel() if hasattr(w, "numel") else 0
+    if w is not None and w.__class__ is not int and w.numel() != known[1]:
+        raise DsmoeError(DSMOE_ERR_INVALID_ARG, where, f"w has {w.numel()} elements, not d_model = {known[1]}")
+    return known[1]
 
 
 def dsmoe_q8_scale_cols(C: int) -> int:
@@ -466,17 +468,21 @@ def dsmoe_q8_scale_cols(C: int) -> int:
     return int(_lib.dsmoe_q8_scale_cols(int(C)))
 
 
+def _scale_cols(C: int) -> int:
+    return 4 * ((C + 511) // 512)
+
+
 def dsmoe_q8_quantize(handle, R, C, x, q, scales, stream=None) -> None:
     where, R, C = "dsmoe_q8_quantize", int(R), int(C)
     p, s = _take(where, handle, stream, ("x", x, "bf16", R * C), ("q", q, "q8", R * C),
-                 ("scales", scales, "q8", R * dsmoe_q8_scale_cols(C)))
+                 ("scales", scales, "q8", R * _scale_cols(C)))
     _check(_lib.dsmoe_q8_quantize(handle, R, C, *p, s), where)
 
 
 def dsmoe_q8_quantize_weights(handle, E, N, K, W, q, scales, stream=None) -> None:
     where, E, N, K = "dsmoe_q8_quantize_weights", int(E), int(N), int(K)
     p, s = _take(where, handle, stream, ("W", W, "bf16", E * N * K), ("q", q, "q8", E * N * K),
-                 ("scales", scales, "q8", E * -(-N // 128) * dsmoe_q8_scale_cols(K)))
+                 ("scales", scales, "q8", E * -(-N // 128) * _scale_cols(K)))
     _check(_lib.dsmoe_q8_quantize_weights(handle, E, N, K, *p, s), where)
 
 
@@ -487,7 +493,7 @@ def dsmoe_norm_q8(handle, T, x, residual, w, eps, r, u, q, scales, stream=None) 
     (x, residual, w, r, u, q, scales), s = _take(
         where, handle, stream, ("x", x, "bf16", n), ("residual", residual, "bf16", n), ("w", w, "bf16", d),
         ("r", r, "bf16", n), ("u", u, "bf16", n), ("q", q, "q8", n),
-        ("scales", scales, "q8", T * dsmoe_q8_scale_cols(d)))
+        ("scales", scales, "q8", T * _scale_cols(d)))
     _check(_lib.dsmoe_norm_q8(handle, T, x, residual, w, float(eps), r, u, q, scales, s), where)
 
 
@@ -503,7 +509,7 @@ def dsmoe_norm_backward(handle, T, dy, dres, r, w, eps, dx, dw, stream=None) -> 
 
 def dsmoe_q8_matmul(handle, E, R, N, K, offsets, a, a_scales, W, W_scales, out, stream=None) -> None:
     where, E, R, N, K = "dsmoe_q8_matmul", int(E), int(R), int(N), int(K)
-    S = dsmoe_q8_scale_cols(K)
+    S = _scale_cols(K)
     p, s = _take(
         where, handle, stream, ("offsets", offsets, "i32", E + 1), ("a", a, "q8", R * K),
         ("a_scales", a_scales, "q8", R * S), ("W", W, "q8", E * N * K),
@@ -514,13 +520,13 @@ def dsmoe_q8_matmul(handle, E, R, N, K, offsets, a, a_scales, W, W_scales, out, 
 def dsmoe_q8_gated_matmul(handle, E, R, N, K, offsets, a, a_scales, W_gate, gate_scales, W_up, up_scales, q, scales,
                           stream=None) -> None:
     where, E, R, N, K = "dsmoe_q8_gated_matmul", int(E), int(R), int(N), int(K)
-    S = dsmoe_q8_scale_cols(K)
+    S = _scale_cols(K)
     nw, ns = E * N * K, E * -(-N // 128) * S
     p, s = _take(
         where, handle, stream, ("offsets", offsets, "i32", E + 1), ("a", a, "q8", R * K),
         ("a_scales", a_scales, "q8", R * S), ("W_gate", W_gate, "q8", nw), ("gate_scales", gate_scales, "q8", ns),
         ("W_up", W_up, "q8", nw), ("up_scales", up_scales, "q8", ns), ("q", q, "q8", R * N),
-        ("scales", scales, "q8", R * dsmoe_q8_scale_cols(N)))
+        ("scales", scales, "q8", R * _scale_cols(N)))
     _check(_lib.dsmoe_q8_gated_matmul(handle, E, R, N, K, *p, s), where)
 
 
@@ -533,7 +539,7 @@ def dsmoe_forward_q8(handle, T, x, x_q, x_scales, residual, token_ids, W_router,
         weights = DsmoeQ8Weights(*[_ptr(t) for n in Q8_WEIGHTS for t in pairs[n]])
     d = _handles[handle][1] if handle in _handles else 0
     n = T * d
-    rows = (("x", x, "bf16", n), ("x_q", x_q, "q8", n), ("x_scales", x_scales, "q8", T * dsmoe_q8_scale_cols(d)),
+    rows = (("x", x, "bf16", n), ("x_q", x_q, "q8", n), ("x_scales", x_scales, "q8", T * _scale_cols(d)),
             ("residual", residual, "bf16", n))
     (x, x_q, x_scales, residual), s = _take(where, handle, stream, *rows)
     st = _lib.dsmoe_forward_q8(handle, T, x, x_q, x_scales, residual, _ptr(token_ids), _ptr(W_router), _ptr(b),
