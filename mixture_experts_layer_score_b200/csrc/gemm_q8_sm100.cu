@@ -76,7 +76,10 @@ struct Geo {
   static constexpr uint32_t kNumBars = 2 * kStages + 2 * kSfSlots + 4 + 1;
   static constexpr uint32_t kOffMisc = kOffBars + kNumBars * 8;
   static constexpr uint32_t kOffTiles = kOffMisc + 32;
-  static constexpr uint32_t kSmemUsed = kOffTiles + (512 + 1) * 4;
+  // the clipped offsets, next to the tile prefix where there is room for them
+  static constexpr bool kRowsInSmem = kTok < 240;
+  static constexpr uint32_t kOffRows = kOffTiles + (512 + 1) * 4;
+  static constexpr uint32_t kSmemUsed = kOffRows + (kRowsInSmem ? (512 + 1) * 4 : 0);
   static constexpr size_t kSmemBytes = kSmemUsed + 1024;  // slack to align the ring to 1024 bytes
   static_assert(kSmemBytes <= 232448, "shared memory budget");
   static_assert(kAccCols <= kSfCol0 && kTok % 16 == 0 && kTok <= 256, "tile geometry");
@@ -169,19 +172,22 @@ struct Q8Tile {
   int expert, row0, m_valid, n_blk;
 };
 
-// Rows [b, t) of group e: offsets clipped to [0, R], empty where they decrease; without offsets
-// all rows.
-__device__ __forceinline__ void group_rows(const Q8GemmArgs& a, int e, int& b, int& t) {
-  if (!a.offsets) {
-    b = 0, t = a.R;
-    return;
-  }
-  b = min(max(__ldg(a.offsets + e), 0), a.R);
-  t = max(min(max(__ldg(a.offsets + e + 1), 0), a.R), b);
+// Offset e, clipped to [0, R]; without offsets all rows are one group's.
+__device__ __forceinline__ int clipped_offset(const Q8GemmArgs& a, int e) {
+  if (!a.offsets) return e == 0 ? 0 : a.R;
+  return min(max(__ldg(a.offsets + e), 0), a.R);
+}
+
+// Rows [b, t) of group e, empty where the offsets decrease.
+template <int kTok>
+__device__ __forceinline__ void group_rows(const Q8GemmArgs& a, const int32_t* rows, int e, int& b, int& t) {
+  b = Geo<kTok>::kRowsInSmem ? rows[e] : clipped_offset(a, e);
+  t = max(Geo<kTok>::kRowsInSmem ? rows[e + 1] : clipped_offset(a, e + 1), b);
 }
 
 template <int kTok>
-__device__ __forceinline__ Q8Tile decode_tile(const Q8GemmArgs& a, const int32_t* tile_start, int tile) {
+__device__ __forceinline__ Q8Tile decode_tile(const Q8GemmArgs& a, const int32_t* tile_start, const int32_t* rows,
+                                              int tile) {
   int lo = 0, hi = a.E - 1;
   while (lo < hi) {  // last group whose first tile is <= tile
     const int mid = (lo + hi + 1) >> 1;
@@ -189,7 +195,7 @@ __device__ __forceinline__ Q8Tile decode_tile(const Q8GemmArgs& a, const int32_t
     else hi = mid - 1;
   }
   int b, e;
-  group_rows(a, lo, b, e);
+  group_rows<kTok>(a, rows, lo, b, e);
   const int M = e - b, mt = (M + kTok - 1) / kTok, local = tile - tile_start[lo], m_blk = local % mt;
   // near-equal token tiles in granules of 16, token tiles fastest: the CTAs that share a
   // weight tile run at the same rate and find it in L2
@@ -288,10 +294,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
   const int kb0 = 4 * kq0, kb1 = kSplit ? min(4 * kq1, kb_all) : kb_all;
   const int tile0 = kSplit ? blockIdx.x / splits : blockIdx.x, tile_step = kSplit ? gridDim.x / splits : gridDim.x;
 
-  for (int e = threadIdx.x; e < a.E; e += kThreads) {
-    int b, t;
-    group_rows(a, e, b, t);
-    tile_start[e + 1] = ((t - b + kTok - 1) / kTok) * n_tiles;
+  int32_t* group_begin = reinterpret_cast<int32_t*>(base + G_::kOffRows);
+  if (G_::kRowsInSmem)
+    for (int e = threadIdx.x; e <= a.E; e += kThreads) group_begin[e] = clipped_offset(a, e);
+  if (threadIdx.x == kThreads - 1) {
+    tma_prefetch_desc(&a.map_a);
+    tma_prefetch_desc(&a.map_w0);
+    if (kGated) tma_prefetch_desc(&a.map_w1);
   }
   if (threadIdx.x == 0) {
     tile_start[0] = 0;
@@ -317,17 +326,22 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
     tmem_relinquish();
   }
   __syncthreads();
-  if (warp == 0) {  // inclusive prefix over tile_start[1..E]
+  if (warp == 0) {  // tile_start[1..E]: the groups' tiles and their inclusive prefix
     int carry = 0;
-    for (int b0 = 1; b0 <= a.E; b0 += 32) {
-      const int i = b0 + lane;
-      int v = (i <= a.E) ? tile_start[i] : 0;
+    for (int b0 = 0; b0 < a.E; b0 += 32) {
+      const int e = b0 + lane;
+      int v = 0;
+      if (e < a.E) {
+        int b, t;
+        group_rows<kTok>(a, group_begin, e, b, t);
+        v = ((t - b + kTok - 1) / kTok) * n_tiles;
+      }
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int n = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += n;
       }
-      if (i <= a.E) tile_start[i] = v + carry;
+      if (e < a.E) tile_start[e + 1] = v + carry;
       carry += __shfl_sync(0xffffffffu, v, 31);
     }
   }
@@ -347,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
       uint32_t phase = 0;
       bool ok = true;
       for (int tile = tile0; ok && tile < total; tile += tile_step) {
-        const Q8Tile t = decode_tile<kTok>(a, tile_start, tile);
+        const Q8Tile t = decode_tile<kTok>(a, tile_start, group_begin, tile);
         const int n0 = t.n_blk * kTileFeat;
         // only the boxes that hold rows of the tile: the copies into shared memory are what
         // bounds the large products
@@ -394,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
     bool ok = true;
     int it = 0;
     for (int tile = tile0; ok && tile < total; tile += tile_step, ++it) {
-      const Q8Tile t = decode_tile<kTok>(a, tile_start, tile);
+      const Q8Tile t = decode_tile<kTok>(a, tile_start, group_begin, tile);
       const int n_mma = (t.m_valid + 15) & ~15;
       const uint32_t idesc = idesc_q8(kFeat, n_mma, 0);
       const int acc = it % G_::kBufs;
@@ -471,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
     uint32_t quad = 0;
     bool ok = true;
     for (int tile = tile0; ok && tile < total; tile += tile_step) {
-      const Q8Tile t = decode_tile<kTok>(a, tile_start, tile);
+      const Q8Tile t = decode_tile<kTok>(a, tile_start, group_begin, tile);
       const int nb0 = kGated ? t.n_blk : 2 * t.n_blk, nb1 = kGated ? nb0 : nb0 + 1;
       const uint32_t* p0 = ws0 + (static_cast<int64_t>(t.expert) * nnb + nb0) * S4;
       const uint32_t* p1 = ws1 + (static_cast<int64_t>(t.expert) * nnb + nb1) * S4;
@@ -520,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
     const int w4 = (warp - 2) & 3;  // this warp's rows of a staged chunk: 4 w4 .. 4 w4 + 3
     int it = 0;
     for (int tile = tile0; tile < total; tile += tile_step, ++it) {
-      const Q8Tile t = decode_tile<kTok>(a, tile_start, tile);
+      const Q8Tile t = decode_tile<kTok>(a, tile_start, group_begin, tile);
       const int acc = it % G_::kBufs;
       if (leader) {
         const bool ok = mbar_wait_checked(&acc_full[acc], (it / G_::kBufs) & 1, a.wait_limit_ns, abort_flag);
@@ -674,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
     __syncwarp();
     pair::cluster_sync();  // the partial sums have arrived
     if (tile0 >= total || warp < 2 || warp >= 2 + kEpiWarps) return;
-    const Q8Tile t = decode_tile<kTok>(a, tile_start, tile0);
+    const Q8Tile t = decode_tile<kTok>(a, tile_start, group_begin, tile0);
     const int slots = kTok / splits;
     for (int slot = warp - 2; slot * splits + rank < t.m_valid; slot += kEpiWarps) {
       float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
