@@ -755,24 +755,24 @@ cudaError_t launch_tok(const Q8GemmArgs& a, int tok, int grid, cudaStream_t s) {
 int64_t token_tiles(int64_t R, int E, int tok) { return (R + (tok - 1) * std::min<int64_t>(E, R)) / tok; }
 }  // namespace
 
-// Token tile by rows per group g = R / E, measured over K = 256 .. 7168 on 32 groups (us, plain
-// N = 4096 or 2048, gated N = 2048):
-//   32   g <= 16 (K = 7168, g = 8: 76.7 against 78.2 with 112; g = 24: 96 against 80), and where
-//        even its tiles are no more than one per SM, each then the shorter (64 groups of 56
-//        rows, N = 128, K = 256, gated: 8.3 against 10.5).
-//   240  one accumulator, so that a tile's epilogue starts are exposed, but an MMA at N = 240
-//        costs 0.5 cycles a token and at N = 112 0.75: from g = 100 on where the K loop is long
-//        enough to bury the start (gated K = 2048, g = 128: 65.8 against 67.6, g = 512: 144
-//        against 172; K = 704, g = 512: 199 against 171 the other way). The plain product's
-//        loop at the same K is as long but its 112-token tiles run two accumulators over a
-//        cheaper epilogue: K >= 4096 (K = 7168, g = 100: 98.8 against 107), or g >= 240 with
-//        g K >= 350,000 (K = 1280, g = 300: 69.0 against 75.9; K = 704, g = 300: 54.5 against
-//        53.1 the other way).
+// Token tile by rows per group g = R / E, measured over K = 256 .. 7168 on 32 groups (us, N = 2048
+// unless said):
+//   32   g <= 16 (plain, K = 7168, g = 8: 76.7 against 78.2 with 112; g = 24: 96 against 80), and
+//        where even its tiles are no more than one per SM, each then the shorter (64 groups of
+//        56 rows, N = 128, K = 256, gated: 8.3 against 10.5).
+//   240  one accumulator, so that the start of a tile's epilogue is exposed, but an MMA at
+//        N = 240 costs 0.5 cycles a token and at N = 112 0.75: from g = 100 on where the K loop is
+//        long enough to bury that start. Gated, K >= 1024 (K = 1024, g = 512: 87 against 99;
+//        K = 2048, g = 120: 62.8 against 67.5; K = 704, g = 300: 61 against 57 the other way).
+//        Plain, whose 112-token tiles run two accumulators over a cheaper epilogue, K >= 4096
+//        (K = 7168, g = 100: 98.8 against 107), or g >= 240 with g K >= 350,000 (K = 1280,
+//        g = 512: 53.8 against 61.1; K = 2048, g = 200: 45.4 against 43.3 and K = 448, g = 512:
+//        35.2 against 33.4 the other way).
 //   112  the rest.
 int q8_token_tile(int64_t R, int E, int N, int K, bool gated, int num_sms) {
   const int64_t n_tiles = gated ? (N + 127) / 128 : (N + 255) / 256, g = R / E;
   if (g <= 16 || std::max<int64_t>(E, (R + 31) / 32) * n_tiles <= num_sms) return 32;
-  const bool large = gated ? g >= 100 && K >= 1280
+  const bool large = gated ? g >= 100 && K >= 1024
                            : (g >= 100 && K >= 4096) || (g >= 240 && g * K >= 350000);
   return large ? 240 : 112;
 }
