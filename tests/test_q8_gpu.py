@@ -357,3 +357,100 @@ def test_wait_limit_runs_out_then_the_handle_recovers(counts, N, K):
     check_gated(h, counts, 0, 0, N, K)
     assert M.dsmoe_get_status(h) == M.DSMOE_OK
     M.dsmoe_destroy(h)
+
+
+# ------------------------------------------------------------------- beyond 32-bit addresses
+LAST = 21  # rows of the end that are checked
+
+
+def test_rows_past_2_31_values():
+    """Rows whose first value lies past 2^31: quantisation, the norm and its backward pass, and a
+    product, each checked at the last rows (the others are zeros)."""
+    d = 8192
+    T = (1 << 31) // d + 5000
+    h = M.dsmoe_create(M.make_cfg(d_model=d, n_routed=1, top_k=1, d_ff=64, max_tokens=T))
+    x = torch.zeros(T, d, dtype=torch.bfloat16, device="cuda")
+    x[-LAST:] = rows(LAST, d, 3)
+    q, s = q8_empty(T, d)
+    M.dsmoe_q8_quantize(h, T, d, x, q, s)
+    eq, es = Q.quantize_rows(NP(x[-LAST:]))
+    np.testing.assert_array_equal(BYTES(q[-LAST:]), eq)
+    np.testing.assert_array_equal(BYTES(s[-LAST:]), es)
+    W = rows(64, d, 4, 0.2).view(1, 64, d)
+    qw, sw, w = q8_weights(W)
+    out = torch.empty(T, 64, dtype=torch.bfloat16, device="cuda")
+    M.dsmoe_q8_matmul(h, 1, T, 64, d, None, q, s, qw, sw, out)
+    a = Q.dequantize_rows(eq, es)
+    y, mag = a @ w[0].T, np.abs(a) @ np.abs(w[0]).T
+    assert (np.abs(NP(out[-LAST:]) - y) <= 2.0 ** -8 * np.abs(y) + (d + 2) * 2.0 ** -23 * mag).all()
+    assert not out[:-LAST].any()
+    wn = (1 + 0.3 * torch.randn(d, generator=torch.Generator().manual_seed(5))).bfloat16().cuda()
+    u = torch.empty_like(x)
+    M.dsmoe_norm_q8(h, T, x, None, wn, EPS, None, u, None, None)
+    eu, rstd = Q.norm(NP(x[-LAST:]), NP(wn), EPS)
+    assert (np.abs(NP(u[-LAST:]) - eu) <= (2.0 ** -8 + 80 * 2.0 ** -24) * np.abs(eu)).all()
+    dy = torch.zeros(T, d, device="cuda")
+    dy[-LAST:] = torch.randn(LAST, d, generator=torch.Generator().manual_seed(6)).cuda()
+    dw = torch.empty(d, device="cuda")
+    M.dsmoe_norm_backward(h, T, dy, None, x, wn, EPS, u, dw)
+    ey, r = NP(dy[-LAST:]), NP(x[-LAST:])
+    ex, ew = Q.norm_backward(ey, None, r, NP(wn), EPS)
+    mag = np.abs(rstd * NP(wn) * ey) + np.abs(r) * rstd ** 3 * np.abs(ey * NP(wn) * r).mean(axis=1, keepdims=True)
+    assert (np.abs(NP(u[-LAST:]) - ex) <= 2.0 ** -8 * np.abs(ex) + 320 * 2.0 ** -24 * mag).all()
+    assert (np.abs(NP(dw) - ew) <= (LAST + 160) * 2.0 ** -24 * np.abs(ey * r * rstd).sum(axis=0)).all()
+    assert M.dsmoe_get_status(h) == M.DSMOE_OK
+    M.dsmoe_destroy(h)
+
+
+def test_weights_past_2_31_values(handle):
+    """The last expert of a weight tensor of more than 2^31 values, plain and gated."""
+    E, N, K, R = 41, 7168, 7424, 40
+    W = torch.zeros(E, N, K, dtype=torch.bfloat16, device="cuda")
+    W[-1] = rows(N, K, 9, 0.2) / 64
+    q = torch.empty(E, N, K, dtype=torch.uint8, device="cuda")
+    s = torch.empty(E, N // 128, M.dsmoe_q8_scale_cols(K), dtype=torch.uint8, device="cuda")
+    M.dsmoe_q8_quantize_weights(handle, E, N, K, W, q, s)
+    eq, es = Q.quantize_weights(NP(W[-1:, -128:]))
+    np.testing.assert_array_equal(BYTES(q[-1:, -128:]), eq)
+    np.testing.assert_array_equal(BYTES(s[-1:, -1:]), es)
+    qa, sa, a = q8_rows(rows(R, K, 2))
+    w = Q.dequantize_weights(eq, es)[0]
+    off = offsets_of([0] * (E - 1) + [R])
+    out = torch.empty(R, N, dtype=torch.bfloat16, device="cuda")
+    M.dsmoe_q8_matmul(handle, E, R, N, K, off, qa, sa, q, s, out)
+    y, mag = a @ w.T, np.abs(a) @ np.abs(w).T
+    err = (K + 2) * 2.0 ** -23 * mag
+    assert (np.abs(NP(out)[:, -128:] - y) <= 2.0 ** -8 * np.abs(y) + err).all()
+    gq, gs = q8_empty(R, N)
+    M.dsmoe_q8_gated_matmul(handle, E, R, N, K, off, qa, sa, q, s, q, s, gq, gs)
+    m = Q.silu(y) * y
+    step = Q.decode_scale(BYTES(gs))[:, N // 128 - 1][:, None]
+    got = Q.decode_e4m3(BYTES(gq)[:, -128:]) * step
+    em = 1.1 * err * np.abs(y) + (np.abs(Q.silu(y)) + 1.1 * err) * err + 2.0 ** -18 * np.abs(m)
+    assert (np.abs(got - m) <= np.maximum(2.0 ** -4 * np.abs(m), 2.0 ** -10 * step) * (1 + 2.0 ** -4) + em).all()
+
+
+# ----------------------------------------------------------------------- two calls at once
+def test_two_handles_on_two_streams():
+    """Products of two handles in flight together give the bits of each alone."""
+    cases = []
+    for i, (counts, N, K) in enumerate((([200, 3, 90], 512, 1040), ([7], 256, 4096), ([30, 300], 384, 704))):
+        h = M.dsmoe_create(M.make_cfg(d_model=64, n_routed=1, top_k=1, d_ff=64, max_tokens=1))
+        E, R = len(counts), sum(counts)
+        qa, sa, _ = q8_rows(rows(R, K, i))
+        qw, sw, _ = q8_weights(rows(E * N, K, i + 9, 0.2).view(E, N, K))
+        out = [torch.empty(R, N, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        cases.append((h, (E, R, N, K, offsets_of(counts), qa, sa, qw, sw), out))
+    torch.cuda.synchronize()
+    for h, a, out in cases:
+        M.dsmoe_q8_matmul(h, *a, out[0])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(20):
+        for (h, a, out), st in zip(cases, streams):
+            M.dsmoe_q8_matmul(h, *a, out[1], st)
+    torch.cuda.synchronize()
+    for h, a, out in cases:
+        assert torch.equal(out[0], out[1])
+        assert M.dsmoe_get_status(h) == M.DSMOE_OK
+        M.dsmoe_destroy(h)
