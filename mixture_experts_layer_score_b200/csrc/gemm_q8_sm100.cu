@@ -21,10 +21,10 @@
 //               memory (32x128b.warpx4) and, per K block, 2 x 4 MMAs of K = 32.
 //   warps 2-9   epilogue: two groups of four warps take alternate 8-token chunks; warp q of
 //               a group reads TMEM lanes [32q, 32q+32) into registers and frees the
-//               accumulator; the group then transposes two chunks at a time through shared
-//               memory so that each output row leaves in one coalesced store. 128
-//               features are one scale block, so the gated output's maximum over a block
-//               is one over a row of the staged chunk.
+//               accumulator. The plain output is stored from there (a warp's pairs of
+//               features make one line of a token's row). The gated output's scale is that
+//               of 128 features, the lanes of four warps: the group transposes two chunks
+//               at a time through shared memory and the maximum is one over a staged row.
 //   warp 10     scale loader: a 32-bit word of a row's scales is four K blocks; the words
 //               of the tile's tokens and of the two weight tiles go to a ring of slots
 //               in the layout that the copy into tensor memory takes.
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
   constexpr bool kGated = kOut == kOutGated;
   constexpr int kTileFeat = kGated ? kFeat : 2 * kFeat;  // output features of a tile
   constexpr int kHold = (kTok / kChunk + 1) / 2;         // chunks of an epilogue group
-  static_assert(kOut != kOutF32 || kTok <= 112, "the fp32 output holds both chains in registers");
+  static_assert(kOut != kOutF32 || G_::kBufs == 2, "the fp32 output leaves the accumulators late");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
   uint8_t* base = smem_raw + pad;
@@ -575,11 +575,42 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
           }
         }
         break;  // a cluster has one tile
+      } else if constexpr (kOut == kOutF32) {
+        // A thread's two accumulators are neighbours in the output row: a warp's words of a token
+        // make one line, stored as they come. What is added is on its way before the
+        // accumulators are read.
+        const int f = n0 + 2 * (q * 32 + lane);
+        const bool on = f < a.N;
+#pragma unroll 1
+        for (int c = half; c < n_chunks; c += 2) {
+          const int n = on ? t.m_valid - kChunk * c : 0;  // tokens of the chunk
+          const int64_t at = static_cast<int64_t>(t.row0 + kChunk * c) * a.N + f;
+          float2 add[kChunk];
+#pragma unroll
+          for (int j = 0; j < kChunk; ++j) {
+            add[j] = make_float2(0.f, 0.f);
+            if (j < n)
+              add[j] = a.add_bf16 ? unpack_bf16x2(*reinterpret_cast<const uint32_t*>(a.add_bf16 + at +
+                                                                                   static_cast<int64_t>(j) * a.N))
+                                  : *reinterpret_cast<const float2*>(a.out_f32 + at + static_cast<int64_t>(j) * a.N);
+          }
+          uint32_t v0[kChunk], v1[kChunk];
+          tmem_ld8(tb + kChunk * c, v0);
+          tmem_ld8(tb + kTok + kChunk * c, v1);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < kChunk; ++j)
+            if (j < n)
+              *reinterpret_cast<float2*>(a.out_f32 + at + static_cast<int64_t>(j) * a.N) =
+                  make_float2(add[j].x + __uint_as_float(v0[j]), add[j].y + __uint_as_float(v1[j]));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[acc]);
       } else {
-        // First the accumulators move to registers (gated: through SwiGLU; bf16: both chains
+        // First the accumulators move to registers (gated: through SwiGLU; plain: both chains
         // rounded into one register), so that the next tile's MMAs may overwrite them ...
-        uint32_t hold[kHold][kChunk], hold1[kOut == kOutF32 ? kHold : 1][kChunk];
-        uint32_t v0[2][kChunk], v1[2][kChunk];
+        uint32_t hold[kHold][kChunk], v0[2][kChunk], v1[2][kChunk];
 #pragma unroll
         for (int i = 0; i < kHold; i += 2) {  // two chunks at a time
           if (2 * i + half >= n_chunks) break;
@@ -595,68 +626,50 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
           for (int j = 0; j < 2 * kChunk; ++j) {
             const int s = j >= kChunk ? 1 : 0;
             if (i + s >= kHold) break;
-            const uint32_t u = v0[s][j & 7], v = v1[s][j & 7];
-            const float x = __uint_as_float(u), y = __uint_as_float(v);
-            if (kGated) hold[i + s][j & 7] = __float_as_uint(swiglu(x, y));
-            else if (kOut == kOutBf16) hold[i + s][j & 7] = pack_bf16x2(x, y);
-            else {
-              hold[i + s][j & 7] = u;
-              hold1[kOut == kOutF32 ? i + s : 0][j & 7] = v;
-            }
+            const float x = __uint_as_float(v0[s][j & 7]), y = __uint_as_float(v1[s][j & 7]);
+            hold[i + s][j & 7] = kGated ? __float_as_uint(swiglu(x, y)) : pack_bf16x2(x, y);
           }
         }
-        tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&acc_empty[acc]);
-        // ... then two chunks at a time are transposed through shared memory and leave row by
-        // row, four rows per warp.
+        if constexpr (!kGated) {
+          // ... then they are stored: a thread's two are neighbours in the output row, and a
+          // warp's words of a token make one line
+          const int f = n0 + 2 * (q * 32 + lane);
+          const int n = f < a.N ? t.m_valid : 0;
+          bf16* out = a.out + static_cast<int64_t>(t.row0) * a.N + f;
 #pragma unroll
-        for (int i = 0; i < kHold; i += 2) {
-          if (2 * i + half >= n_chunks) break;
-          uint32_t* st = reinterpret_cast<uint32_t*>(stg + (kOut == kOutF32 ? 0 : buf * kStgBytes));
-          if (kOut == kOutF32) group_sync(half);  // both buffers are one, and free
+          for (int i = 0; i < kHold; ++i) {
+            const int tok = kChunk * (2 * i + half);
+            if (tok >= t.m_valid) break;
 #pragma unroll
-          for (int j = 0; j < 2 * kChunk; ++j) {
-            const int ii = i + (j >= kChunk ? 1 : 0);
-            if (ii >= kHold) break;
-            const uint32_t v = hold[ii][j & 7];  // gated: feature 32 q + lane; else two features
-            if (kOut != kOutF32) st[j * kFeat + q * 32 + lane] = v;
-            else
-              reinterpret_cast<uint2*>(st)[j * kFeat + q * 32 + lane] =
-                  make_uint2(v, hold1[kOut == kOutF32 ? ii : 0][j & 7]);
+            for (int j = 0; j < kChunk; ++j)
+              if (tok + j < n) *reinterpret_cast<uint32_t*>(out + static_cast<int64_t>(tok + j) * a.N) = hold[i][j];
           }
-          group_sync(half);
-          // this warp's four rows of the sixteen, neighbours in the output
-          const int j0 = 4 * w4, tok = kChunk * (2 * (i + (j0 >= kChunk ? 1 : 0)) + half) + (j0 & (kChunk - 1));
-          const int n_rows = t.m_valid - tok;
-          const int64_t row = t.row0 + tok;
-          if (kGated) {
+        } else {
+          // ... then two chunks at a time are transposed through shared memory (a scale is that of
+          // 128 features, four warps' lanes) and leave row by row, four rows per warp
+#pragma unroll
+          for (int i = 0; i < kHold; i += 2) {
+            if (2 * i + half >= n_chunks) break;
+            uint32_t* st = reinterpret_cast<uint32_t*>(stg + buf * kStgBytes);
+#pragma unroll
+            for (int j = 0; j < 2 * kChunk; ++j) {
+              const int ii = i + (j >= kChunk ? 1 : 0);
+              if (ii >= kHold) break;
+              st[j * kFeat + q * 32 + lane] = hold[ii][j & 7];
+            }
+            group_sync(half);
+            // this warp's four rows of the sixteen, neighbours in the output
+            const int j0 = 4 * w4, tok = kChunk * (2 * (i + (j0 >= kChunk ? 1 : 0)) + half) + (j0 & (kChunk - 1));
             float4 m[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) m[r] = reinterpret_cast<const float4*>(st)[(j0 + r) * (kFeat / 4) + lane];
-            if (n_rows > 0) store_gated_rows<4>(a, row, min(n_rows, 4), t.n_blk, lane, m);
-          } else if (kOut == kOutBf16) {
-            const int f = n0 + 8 * lane;
-            uint4 o[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) o[r] = reinterpret_cast<const uint4*>(st)[(j0 + r) * (2 * kFeat / 8) + lane];
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (r < n_rows && f < a.N)
-                *reinterpret_cast<uint4*>(a.out + row * a.N + f + static_cast<int64_t>(r) * a.N) = o[r];
-          } else {
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-              for (int ch = 0; ch < 2; ++ch) {
-                const int f = n0 + ch * kFeat + 4 * lane;
-                if (r < n_rows && f < a.N)
-                  add_f32(a, (row + r) * a.N + f,
-                          reinterpret_cast<const float4*>(st)[(j0 + r) * (2 * kFeat / 4) + ch * 32 + lane]);
-              }
+            if (tok < t.m_valid)
+              store_gated_rows<4>(a, t.row0 + tok, min(t.m_valid - tok, 4), t.n_blk, lane, m);
+            buf ^= 1u;
           }
-          if (kOut != kOutF32) buf ^= 1u;
         }
       }
     }
