@@ -578,7 +578,8 @@ dsmoe_status dsmoe_q8_quantize_weights(dsmoe_handle* h, int32_t E, int32_t N, in
 /*
  * The root-mean-square norm in front of the layer, for T <= max_tokens rows of d = d_model:
  *   r = bf16(x + residual), u = bf16(r w / sqrt(mean(r^2) + eps)), and the 8-bit rows of u
- * (statistics in fp32; the 8-bit rows are exactly dsmoe_q8_quantize of u).
+ * (the row's sum of squares in fp32, which it must not overflow; the 8-bit rows are exactly
+ * dsmoe_q8_quantize of u).
  *
  * dsmoe_norm_q8
  *     x         bf16 [T, d]

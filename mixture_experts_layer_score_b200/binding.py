@@ -649,7 +649,8 @@ class DSMoE:
 class DSMoEQ8(DSMoE):
     """The layer with its expert weights in 8 bits. weights: DSMoE's dict; the six expert tensors
     may be bf16 (quantised here, once; the bf16 tensors are not kept) or (values, scales)
-    pairs that already are in 8 bits."""
+    pairs that already are in 8 bits. sharded.expert_sharded_forward takes it as it takes a
+    DSMoE; the token-dispatch form and the backward pass need the bf16 weights."""
 
     def __init__(self, cfg: DsmoeCfg, weights: Dict, device: int = 0):
         import torch

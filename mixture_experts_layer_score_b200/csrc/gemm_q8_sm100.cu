@@ -30,10 +30,18 @@
 //               in the layout that the copy into tensor memory takes.
 // Every wait is bounded; a role that gives up raises the abort flag and a status bit, the
 // CTA drains its copies and MMAs and returns; the epilogue's groups decide together (through
-// shared memory), so that none of their barriers is left waiting. Where a launch has few tiles (few rows, few
-// features), the CTAs of a cluster share a tile along K: each sends its fp32 partial sums
-// through distributed shared memory to the CTA that owns the token, which adds them in the
-// order of K.
+// shared memory), so that none of their barriers is left waiting. Where a launch has few
+// tiles (few rows, few features), the CTAs of a cluster share a tile along K: each sends its
+// fp32 partial sums through distributed shared memory to the CTA that owns the token, which
+// adds them in the order of K.
+//
+// What bounds it: with few rows the weights' bytes (48 experts of 7168 x 2048 and 144 rows: 109 us,
+// 6.3 TB/s); with many the power limit (gate/up, 8192 rows, 32 experts, d = 7168, F = 2048:
+// 250-270 us in a burst, 287-310 repeated at 990 W and 1.2-1.4 GHz, 1.6-1.8 PFLOP/s); with a short K
+// loop a tile's start and end (32,768 rows, 64 experts, K = 704, N = 1024: 45 us, floor 21).
+// An MMA of M = 128, K = 32 takes max(64 + 0.14 N, N / 2) cycles, hence the large N.
+// The accumulation over K is the tensor core's: fp32, truncating (relative error 4e-7 at
+// K = 7168).
 #include <algorithm>
 
 #include "kernels.h"
@@ -211,7 +219,7 @@ __device__ __forceinline__ Q8Tile decode_tile(const Q8GemmArgs& a, const int32_t
 
 // SiLU(g) u. The approximations that flush subnormals take half the instructions of those that
 // do not, and the drain of a gated tile is bound by its instructions; what they flush is
-// nothing here: e^-g next to 1, and 1 / (1 + e^-g) below 2^-126 (g < -87).
+// e^-g next to 1, and 1 / (1 + e^-g) below 2^-126 (g < -87, where |SiLU| < 1.1e-36 becomes 0).
 __device__ __forceinline__ float swiglu(float g, float u) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
@@ -363,8 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
       for (int tile = tile0; ok && tile < total; tile += tile_step) {
         const Q8Tile t = decode_tile<kTok>(a, tile_start, group_begin, tile);
         const int n0 = t.n_blk * kTileFeat;
-        // only the boxes that hold rows of the tile: the copies into shared memory are what
-        // bounds the large products
+        // only the boxes that hold rows of the tile (a full tile's bytes every time: 342 us for
+        // the large gate/up, 329 so)
         const int boxes = (t.m_valid + G_::kBoxRows - 1) / G_::kBoxRows;
         const uint32_t stage_bytes = kWBytes + boxes * G_::kBoxRows * kBK;
         for (int kb = kb0; kb < kb1; ++kb) {

@@ -45,7 +45,7 @@ __device__ __forceinline__ uint32_t half_warp_max(uint32_t v) {
 }
 
 // Sixteen lanes hold one block of 128 values, eight each; every thread has kQuantUnits blocks in
-// flight.
+// flight (8192 x 7168: 57 us with one, 36 with two or four, 41 with eight).
 constexpr int kQuantUnits = 4;
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const bf16* __restrict__ x, uint32_t units, int C,
                                                             uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
@@ -214,7 +214,8 @@ __device__ __forceinline__ uint4 add_bf16x8(const uint4& a, const uint4& b) {
 // One row at a time per block, 8 NV values per thread: r = bf16(x + residual) stays in
 // registers between the sum of squares and the scaled row u = bf16((r rstd) w); the 8-bit
 // row is that of u, so that it equals the quantisation of the bf16 row. The block loads
-// its next row before it reduces this one.
+// its next row before it reduces this one. Bound by HBM: 9 bytes a value, 8192 x 7168 in
+// 85-88 us (6.1 TB/s).
 template <int NV>
 __global__ void __launch_bounds__(NV == 1 ? 256 : 512) norm_q8_kernel(const NormArgs a) {
   __shared__ __align__(16) float red[2][32];
@@ -315,9 +316,11 @@ __device__ __forceinline__ void store_share(float* part, int64_t at, const float
 }
 
 // dx and this block's share of dw, for rows of at most 8192 values: eight columns per
-// thread, rows t, t + grid, ... in order. The rows ahead are copied into a ring of kStages
+// thread, rows t, t + grid, ... in order. The rows ahead are copied into a ring of kBwdStages
 // rows in shared memory, so that loads stay in flight through the barrier of the row's sums
-// (of r^2 and of w dy r); each warp reads only what it copied itself.
+// (of r^2 and of w dy r); each warp reads only what it copied itself. Bound by HBM: 10 bytes a
+// value, 16384 x 1280 in 37 us with the kernel that adds the shares (49 us with the rows
+// loaded into registers between the barriers).
 constexpr int kBwdStages = 3;
 __global__ void __launch_bounds__(1024) norm_backward_kernel(const NormBwdArgs a) {
   extern __shared__ __align__(16) uint4 ring[];
