@@ -2024,8 +2024,9 @@ DSMOE_EXPORT dsmoe_status dsmoe_norm_backward(dsmoe_handle* h, int32_t T, const 
   a.d = h->cfg.d_model;
   a.dx = static_cast<bf16*>(dx);
   a.part = h->norm_part;
-  CUDA_TRY(dsmoe::launch_norm_backward(a, dw, h->num_sms, s));
-  h->launches += 2;
+  int launches = 0;
+  CUDA_TRY(dsmoe::launch_norm_backward(a, dw, h->num_sms, s, &launches));
+  h->launches += launches;
   return DSMOE_OK;
 }
 

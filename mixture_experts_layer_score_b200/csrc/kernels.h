@@ -340,7 +340,7 @@ struct NormBwdArgs {
 };
 constexpr int kNormMaxSms = 192;  // SMs that the partial sums are sized for
 int norm_backward_blocks(int64_t T, int d, int num_sms);
-cudaError_t launch_norm_backward(const NormBwdArgs& a, float* dw, int num_sms, cudaStream_t s);
+cudaError_t launch_norm_backward(const NormBwdArgs& a, float* dw, int num_sms, cudaStream_t s, int* launches);
 
 // Grouped products of 8-bit rows with 8-bit weights (gemm_q8_sm100.cu): rows offsets[e] ..
 // offsets[e+1] of a [R, K] times expert e's W [N, K]. One of three outputs: `out` bf16;

@@ -120,7 +120,8 @@ def test_norm(T, d, with_residual):
     M.dsmoe_destroy(h)
 
 
-@pytest.mark.parametrize("T,d", NORM + [(1500, 128)])
+# (up to four rows one block adds dw itself, beyond that a second kernel does)
+@pytest.mark.parametrize("T,d", NORM + [(1500, 128), (4, 1024), (5, 1024), (2, 7168), (20, 64)])
 @pytest.mark.parametrize("with_dres", [False, True])
 def test_norm_backward(T, d, with_dres):
     h = M.dsmoe_create(M.make_cfg(d_model=d, n_routed=1, top_k=1, d_ff=64, max_tokens=T + 3))
