@@ -274,6 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
   constexpr int kTileFeat = kGated ? kFeat : 2 * kFeat;  // output features of a tile
   constexpr int kHold = (kTok / kChunk + 1) / 2;         // chunks of an epilogue group
   static_assert(kOut != kOutF32 || G_::kBufs == 2, "the fp32 output leaves the accumulators late");
+  static_assert(!kSplit || (kTok % 8 == 0 && kTok * 2 * kFeat * 4 <= G_::kOffSf), "the ring holds the partial sums");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
   uint8_t* base = smem_raw + pad;
@@ -561,28 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
       const int n_chunks = (t.m_valid + kChunk - 1) / kChunk;
       const int n0 = t.n_blk * kTileFeat;
       if constexpr (kSplit) {
-        // the partial sums of token t go to CTA t % splits, slot t / splits, where part
-        // [source CTA][slot][chain][feature] of the staging area waits for them
-#pragma unroll
-        for (int i = 0; i < kHold; ++i) {
-          const int c = 2 * i + half;
-          if (c >= n_chunks) break;
-          uint32_t p0[kChunk], p1[kChunk];
-          tmem_ld8(tb + kChunk * c, p0);
-          tmem_ld8(tb + kTok + kChunk * c, p1);
-          tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < kChunk; ++j) {
-            const int tok = kChunk * c + j;
-            if (tok >= t.m_valid) break;
-            const uint32_t at = smem_addr(base + G_::kOffStg) +
-                                ((rank * (kTok / splits) + tok / splits) * 2 * kFeat + q * 32 + lane) * 4;
-            const uint32_t to = pair::map_to(at, tok % splits);
-            pair::st_cluster_u32(to, p0[j]);
-            pair::st_cluster_u32(to + kFeat * 4, p1[j]);
-          }
-        }
-        break;  // a cluster has one tile
+        break;  // a cluster has one tile, joined below
       } else if constexpr (kOut == kOutF32) {
         // A thread's two accumulators are neighbours in the output row: a warp's words of a token
         // make one line, stored as they come. What is added is on its way before the
@@ -699,13 +679,45 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
         atomicOr(a.status, kStatusTimeoutDrain);
     }
   }
+  if constexpr (kSplit) {
+    // The partial sums of token t go to CTA t % splits, slot t / splits, to the place
+    // [source CTA][slot][chain][feature] of its ring, which nothing uses any more once every
+    // CTA of the cluster is here.
+    __syncthreads();
+    pair::cluster_sync();
+    const bool epilogue = warp >= 2 && warp < 2 + kEpiWarps && tile0 < total;
+    if (epilogue && !*abort_flag) {
+      const Q8Tile t = decode_tile<kTok>(a, tile_start, group_begin, tile0);
+      tc_fence_after();
+      const int q = warp & 3;
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll 1
+      for (int c = (warp - 2) >> 2; kChunk * c < t.m_valid; c += 2) {
+        uint32_t p0[kChunk], p1[kChunk];
+        tmem_ld8(tb + kChunk * c, p0);
+        tmem_ld8(tb + kTok + kChunk * c, p1);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) {
+          const int tok = kChunk * c + j;
+          if (tok >= t.m_valid) break;
+          const uint32_t at =
+              smem_addr(base) + ((rank * (kTok / splits) + tok / splits) * 2 * kFeat + q * 32 + lane) * 4;
+          const uint32_t to = pair::map_to(at, tok % splits);
+          pair::st_cluster_u32(to, p0[j]);
+          pair::st_cluster_u32(to + kFeat * 4, p1[j]);
+        }
+      }
+    }
+    __syncwarp();
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, kTmemCols);
   }
-  if (kSplit) {
+  if constexpr (kSplit) {
     __syncwarp();
     pair::cluster_sync();  // the partial sums have arrived
     if (tile0 >= total || warp < 2 || warp >= 2 + kEpiWarps) return;
@@ -714,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
     for (int slot = warp - 2; slot * splits + rank < t.m_valid; slot += kEpiWarps) {
       float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
       for (int s = 0; s < splits; ++s) {  // in the order of K
-        const float4* p = reinterpret_cast<const float4*>(base + G_::kOffStg) + (s * slots + slot) * (kFeat / 2) + lane;
+        const float4* p = reinterpret_cast<const float4*>(base) + (s * slots + slot) * (kFeat / 2) + lane;
         const float4 x = p[0], y = p[kFeat / 4];
         g.x += x.x, g.y += x.y, g.z += x.z, g.w += x.w;
         u.x += y.x, u.y += y.y, u.z += y.z, u.w += y.w;
@@ -765,7 +777,7 @@ cudaError_t launch_one(const Q8GemmArgs& a, int grid, cudaStream_t s) {
 
 template <int kOut>
 cudaError_t launch_tok(const Q8GemmArgs& a, int tok, int grid, cudaStream_t s) {
-  if (a.splits > 1) return launch_one<kOut, 32, true>(a, grid, s);
+  if (a.splits > 1) return tok == 32 ? launch_one<kOut, 32, true>(a, grid, s) : launch_one<kOut, 112, true>(a, grid, s);
   if (tok == 32) return launch_one<kOut, 32, false>(a, grid, s);
   if constexpr (kOut != kOutF32)
     if (tok == 240) return launch_one<kOut, 240, false>(a, grid, s);
@@ -789,24 +801,36 @@ int64_t token_tiles(int64_t R, int E, int tok) { return (R + (tok - 1) * std::mi
 //        (K = 7168, g = 100: 98.8 against 107), or g >= 240 with g K >= 350,000 (K = 1280,
 //        g = 512: 53.8 against 61.1; K = 2048, g = 200: 45.4 against 43.3 and K = 448, g = 512:
 //        35.2 against 33.4 the other way).
-//   112  the rest.
+//   112  the rest, and in place of 32 where its clusters (q8_splits) shorten a CTA's K loop by 14
+//        blocks or more (128 rows, gated, K = 7168: 18.7 against 22.3; 256 rows: 26.9 against 30.5;
+//        4 groups of 169 rows, N = 600, K = 3968: 16.6 against 18.7; 13 blocks, 5 groups of 184 rows,
+//        K = 3280, gated: 21.7 against 18.6 the other way).
+static int q8_splits(int64_t tiles, int tok, int K, int num_sms);
 int q8_token_tile(int64_t R, int E, int N, int K, bool gated, int num_sms) {
   const int64_t n_tiles = gated ? (N + 127) / 128 : (N + 255) / 256, g = R / E;
-  if (g <= 16 || std::max<int64_t>(E, (R + 31) / 32) * n_tiles <= num_sms) return 32;
+  if (g <= 16) return 32;
+  if (std::max<int64_t>(E, (R + 31) / 32) * n_tiles <= num_sms) {
+    const int kb = (K + kBK - 1) / kBK;
+    const int s32 = q8_splits(token_tiles(R, E, 32) * n_tiles, 32, K, num_sms);
+    const int s112 = q8_splits(token_tiles(R, E, 112) * n_tiles, 112, K, num_sms);
+    return kb / s32 - kb / s112 >= 14 ? 112 : 32;
+  }
   const bool large = gated ? g >= 100 && K >= 1024
                            : (g >= 100 && K >= 4096) || (g >= 240 && g * K >= 350000);
   return large ? 240 : 112;
 }
 
-// CTAs that share a 32-token tile along K: the most of 8, 4, 2 whose clusters run side by side
-// (of 148 SMs, 15 clusters of 8 CTAs, 33 of 4, 74 of 2) and that leave each CTA a group of
-// four K blocks. One row, N = 128, K = 7168, gated: 28.4 us alone, 18.7, 14.0 and 10.5 with
-// 2, 4 and 8; 16 tiles: 28.9, 18.7, 14.6 and 18.8 (the 16th cluster of 8 runs afterwards).
-static int q8_splits(int64_t tiles, int K, int num_sms) {
-  const int groups = (K + 511) / 512;
+// CTAs that share a tile along K: the most of 8, 4, 2 whose clusters run side by side (of 148 SMs,
+// 15 clusters of 8 CTAs, 33 of 4, 74 of 2) and that leave each CTA a group of four K blocks.
+// One row, N = 128, K = 7168, gated: 28.4 us alone, 18.7, 14.0 and 10.5 with 2, 4 and 8; 16 tiles:
+// 28.9, 18.7, 14.6 and 18.8 (the 16th cluster of 8 runs afterwards). Joining the sums of a
+// 112-token tile takes longer, so there the K loop has to get 14 blocks shorter.
+static int q8_splits(int64_t tiles, int tok, int K, int num_sms) {
+  const int groups = (K + 511) / 512, kb = (K + kBK - 1) / kBK;
+  if (tok > 112) return 1;
   for (int s = 8; s > 1; s >>= 1) {
     const int idle = s == 8 ? 28 : s == 4 ? 16 : 0;
-    if (tiles * s <= num_sms - idle && groups >= s) return s;
+    if (tiles * s <= num_sms - idle && groups >= s) return tok == 32 || kb - kb / s >= 14 ? s : 1;
   }
   return 1;
 }
@@ -816,7 +840,7 @@ cudaError_t launch_gemm_q8(const Q8GemmArgs& args, int tok, int num_sms, cudaStr
   const bool gated = a.q_out != nullptr;
   const int64_t n_tiles = (a.N + (gated ? 127 : 255)) / (gated ? 128 : 256);
   const int64_t bound = token_tiles(a.R, a.E, tok) * n_tiles;
-  a.splits = tok == 32 ? q8_splits(bound, a.K, num_sms) : 1;
+  a.splits = q8_splits(bound, tok, a.K, num_sms);
   const int grid = static_cast<int>(a.splits > 1 ? bound * a.splits : std::min<int64_t>(bound, num_sms));
   if (gated) return launch_tok<kOutGated>(a, tok, grid, s);
   return a.out_f32 ? launch_tok<kOutF32>(a, tok, grid, s) : launch_tok<kOutBf16>(a, tok, grid, s);

@@ -169,6 +169,9 @@ PRODUCTS = [  # counts of each expert, first row, rows behind the last, N, K
     ([1], 1, 1, 776, 4624),
     ([32], 0, 0, 2048, 2064),
     ([0, 40, 3], 0, 2, 520, 1552),
+    # ... of 112-token tiles
+    ([128], 0, 0, 2048, 7168),
+    ([111, 113, 160, 224], 1, 3, 600, 3968),
 ]
 
 
