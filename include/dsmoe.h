@@ -561,8 +561,9 @@ dsmoe_status dsmoe_route_noalloc(const dsmoe_cfg* cfg, int32_t T, const void* x,
  *   rows     values [R, C], scales [R, S(C)]
  *   weights  values [E, N, K], scales [E, ceil(N / 128), S(K)]
  *
- * Sizes: C and K multiples of 16, at most 32768; E at most 512; R at most 2^30. All device
- * pointers are 16-byte aligned and outputs must not overlap inputs unless said. The handle
+ * Sizes: C and K multiples of 16, at most 32768; E at most 512; R at most 2^30. Device
+ * pointers are 16-byte aligned, those of scales and offsets 4-byte (so that slices of rows
+ * or of experts may be passed); outputs must not overlap inputs unless said. The handle
  * gives the device, the status word and the wait limit; except where d or T is named, its
  * configuration does not matter.
  *

@@ -1879,6 +1879,17 @@ dsmoe_status check_pointers(std::initializer_list<const void*> ptrs) {
   return DSMOE_OK;
 }
 
+// Scales are read and written in words and bytes: 4-byte alignment (a slice of rows or of experts
+// has no more where a row has one word of scales).
+dsmoe_status check_scales(std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs) {
+    if (!p) return fail(DSMOE_ERR_INVALID_ARG, "NULL argument");
+    if (reinterpret_cast<uintptr_t>(p) & 3u)
+      return fail(DSMOE_ERR_INVALID_ARG, "scales pointer %p is not 4-byte aligned", p);
+  }
+  return DSMOE_OK;
+}
+
 constexpr int kQ8MaxDim = 32768;       // as d_model and d_ff
 constexpr int64_t kQ8MaxRows = 1 << 30;  // as max_tokens * top_k
 
@@ -1943,7 +1954,8 @@ DSMOE_EXPORT dsmoe_status dsmoe_q8_quantize(dsmoe_handle* h, int64_t R, int32_t 
   if (!h) return fail(DSMOE_ERR_INVALID_ARG, "handle is NULL");
   STAGE_TRY(check_q8_dims(R, 1, 1, C, 1));
   if (R == 0) return DSMOE_OK;
-  STAGE_TRY(check_pointers({x, q, scales}));
+  STAGE_TRY(check_pointers({x, q}));
+  STAGE_TRY(check_scales({scales}));
   DeviceGuard g(h->device);
   if (!g.ok) return fail(DSMOE_ERR_CUDA, "cannot select device %d", h->device);
   CUDA_TRY(dsmoe::launch_quantize_rows(static_cast<const bf16*>(x), R, C, static_cast<uint8_t*>(q),
@@ -1956,7 +1968,8 @@ DSMOE_EXPORT dsmoe_status dsmoe_q8_quantize_weights(dsmoe_handle* h, int32_t E, 
                                                     void* q, void* scales, void* stream) {
   if (!h) return fail(DSMOE_ERR_INVALID_ARG, "handle is NULL");
   STAGE_TRY(check_q8_dims(0, E, N, K, 1));
-  STAGE_TRY(check_pointers({W, q, scales}));
+  STAGE_TRY(check_pointers({W, q}));
+  STAGE_TRY(check_scales({scales}));
   DeviceGuard g(h->device);
   if (!g.ok) return fail(DSMOE_ERR_CUDA, "cannot select device %d", h->device);
   CUDA_TRY(dsmoe::launch_quantize_weights(static_cast<const bf16*>(W), E, N, K, static_cast<uint8_t*>(q),
@@ -1977,8 +1990,9 @@ DSMOE_EXPORT dsmoe_status dsmoe_norm_q8(dsmoe_handle* h, int32_t T, const void* 
   if (T == 0) return DSMOE_OK;
   STAGE_TRY(check_pointers({x, w}));
   for (const void* p : {residual, static_cast<const void*>(r), static_cast<const void*>(u),
-                        static_cast<const void*>(q), static_cast<const void*>(scales)})
+                        static_cast<const void*>(q)})
     if (p && !aligned16(p)) return fail(DSMOE_ERR_INVALID_ARG, "pointer %p is not 16-byte aligned", p);
+  if (scales) STAGE_TRY(check_scales({scales}));
   DeviceGuard g(h->device);
   if (!g.ok) return fail(DSMOE_ERR_CUDA, "cannot select device %d", h->device);
   dsmoe::NormArgs a;
@@ -2037,7 +2051,8 @@ DSMOE_EXPORT dsmoe_status dsmoe_q8_matmul(dsmoe_handle* h, int32_t E, int64_t R,
   STAGE_TRY(check_q8_dims(R, E, N, K, 8));
   if (!offsets && E != 1) return fail(DSMOE_ERR_INVALID_ARG, "offsets is required for E = %d", E);
   if (R == 0) return DSMOE_OK;
-  STAGE_TRY(check_pointers({a, a_scales, W, W_scales, out}));
+  STAGE_TRY(check_pointers({a, W, out}));
+  STAGE_TRY(check_scales({a_scales, W_scales}));
   DeviceGuard g(h->device);
   if (!g.ok) return fail(DSMOE_ERR_CUDA, "cannot select device %d", h->device);
   Q8Out o;
@@ -2054,7 +2069,8 @@ DSMOE_EXPORT dsmoe_status dsmoe_q8_gated_matmul(dsmoe_handle* h, int32_t E, int6
   STAGE_TRY(check_q8_dims(R, E, N, K, 16));
   if (!offsets && E != 1) return fail(DSMOE_ERR_INVALID_ARG, "offsets is required for E = %d", E);
   if (R == 0) return DSMOE_OK;
-  STAGE_TRY(check_pointers({a, a_scales, W_gate, gate_scales, W_up, up_scales, q, scales}));
+  STAGE_TRY(check_pointers({a, W_gate, W_up, q}));
+  STAGE_TRY(check_scales({a_scales, gate_scales, up_scales, scales}));
   DeviceGuard g(h->device);
   if (!g.ok) return fail(DSMOE_ERR_CUDA, "cannot select device %d", h->device);
   const Q8Rows up{W_up, up_scales};
@@ -2077,9 +2093,12 @@ dsmoe_status check_forward_q8(dsmoe_handle* h, const FwdQ8Args& a) {
   if (st != DSMOE_OK || a.f.T == 0) return st;
   if (!a.w) return fail(DSMOE_ERR_INVALID_ARG, "weights is NULL");
   const dsmoe_q8_weights& w = *a.w;
-  st = check_pointers({a.xq, a.xs, a.f.h, w.W_gate, w.W_gate_scales, w.W_up, w.W_up_scales, w.W_down, w.W_down_scales});
-  if (st == DSMOE_OK && h->add_shared && h->cfg.n_shared > 0)
-    st = check_pointers({w.Ws_gate, w.Ws_gate_scales, w.Ws_up, w.Ws_up_scales, w.Ws_down, w.Ws_down_scales});
+  st = check_pointers({a.xq, a.f.h, w.W_gate, w.W_up, w.W_down});
+  if (st == DSMOE_OK) st = check_scales({a.xs, w.W_gate_scales, w.W_up_scales, w.W_down_scales});
+  if (st == DSMOE_OK && h->add_shared && h->cfg.n_shared > 0) {
+    st = check_pointers({w.Ws_gate, w.Ws_up, w.Ws_down});
+    if (st == DSMOE_OK) st = check_scales({w.Ws_gate_scales, w.Ws_up_scales, w.Ws_down_scales});
+  }
   if (st != DSMOE_OK) return st;
   if (a.residual && !aligned16(a.residual))
     return fail(DSMOE_ERR_INVALID_ARG, "pointer %p is not 16-byte aligned", a.residual);

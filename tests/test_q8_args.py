@@ -60,7 +60,7 @@ class TestHandle:
         assert self.status(lambda: M.dsmoe_q8_quantize(self.h, R, C, 16, 16, 16, 0)) == expect
 
     @pytest.mark.parametrize("x,q,s", [(None, 16, 16), (16, None, 16), (16, 16, None), (8, 16, 16), (16, 24, 16),
-                                       (16, 16, 4)])
+                                       (16, 16, 6)])
     def test_quantize_pointers(self, x, q, s):
         assert self.status(lambda: M.dsmoe_q8_quantize(self.h, 1, 16, x, q, s, 0)) == 1
 
@@ -73,7 +73,8 @@ class TestHandle:
         ok = dict(T=1, x=16, res=None, w=16, eps=1e-6, r=None, u=16, q=None, s=None)
         for bad, expect in ((dict(T=-1), 1), (dict(T=9), 3), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1),
                             (dict(eps=float("inf")), 1), (dict(q=16), 1), (dict(s=16), 1), (dict(u=None), 1),
-                            (dict(x=None), 1), (dict(w=None), 1), (dict(x=8), 1), (dict(res=8), 1), (dict(u=8), 1)):
+                            (dict(x=None), 1), (dict(w=None), 1), (dict(x=8), 1), (dict(res=8), 1), (dict(u=8), 1),
+                            (dict(q=8, s=16), 1), (dict(q=16, s=18), 1)):
             a = ok | bad
             assert self.status(lambda: M.dsmoe_norm_q8(self.h, a["T"], a["x"], a["res"], a["w"], a["eps"], a["r"],
                                                        a["u"], a["q"], a["s"], 0)) == expect, bad
@@ -102,11 +103,16 @@ class TestHandle:
 
     def test_product_pointers(self):
         for i in range(6):
-            for bad in ((None, 8) if i else (None,)):  # (offsets may only be NULL where E is 1)
+            for bad in ((None, 6) if i else (None,)):  # (offsets may only be NULL where E is 1)
                 p = [16] * 6
                 p[i] = bad
                 assert self.status(lambda: M.dsmoe_q8_matmul(self.h, 2, 1, 8, 16, *p, 0)) == 1
         for i in range(9):
-            p = [16] * 9
-            p[i] = None
-            assert self.status(lambda: M.dsmoe_q8_gated_matmul(self.h, 2, 1, 16, 16, *p, 0)) == 1
+            for bad in ((None, 6) if i else (None,)):
+                p = [16] * 9
+                p[i] = bad
+                assert self.status(lambda: M.dsmoe_q8_gated_matmul(self.h, 2, 1, 16, 16, *p, 0)) == 1
+        for i in (1, 3, 5):  # values need 16 bytes
+            p = [16] * 6
+            p[i] = 8
+            assert self.status(lambda: M.dsmoe_q8_matmul(self.h, 2, 1, 8, 16, *p, 0)) == 1

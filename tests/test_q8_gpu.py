@@ -434,6 +434,34 @@ def test_weights_past_2_31_values(handle):
     assert (np.abs(got - m) <= np.maximum(2.0 ** -4 * np.abs(m), 2.0 ** -10 * step) * (1 + 2.0 ** -4) + em).all()
 
 
+def test_slices_of_rows_and_experts(handle):
+    """Slices as they come: rows from the third on and experts from the second on, whose scales are
+    only 4-byte aligned (one word of scales per row), and 8-bit rows written into a slice."""
+    E, N, K, R = 3, 48, 144, 30
+    qa, sa, a = q8_rows(rows(R, K, 1))
+    qw, sw, w = q8_weights(rows(E * N, K, 2, 0.2).view(E, N, K))
+    assert sa.shape[1] == 4 and sw[1:].data_ptr() % 16 == 4
+    out = torch.empty(R - 3, N, dtype=torch.bfloat16, device="cuda")
+    off = offsets_of([20, 7])
+    M.dsmoe_q8_matmul(handle, E - 1, R - 3, N, K, off, qa[3:], sa[3:], qw[1:], sw[1:], out)
+    o = [0, 20, 27]
+    y, mag = Q.grouped(a[3:], w[1:], o), Q.grouped(np.abs(a[3:]), np.abs(w[1:]), o)
+    assert (np.abs(NP(out) - y) <= 2.0 ** -8 * np.abs(y) + (K + 2) * 2.0 ** -23 * mag).all()
+    q, s = q8_empty(R, N)
+    q.view(torch.uint8).fill_(9)
+    s.view(torch.uint8).fill_(9)
+    M.dsmoe_q8_gated_matmul(handle, E - 1, R - 3, N, K, off, qa[3:], sa[3:], qw[1:], sw[1:], qw[1:], sw[1:], q[3:],
+                            s[3:])
+    assert (BYTES(q)[:3] == 9).all() and (BYTES(s)[:3] == 9).all()
+    m = Q.silu(y) * y
+    assert np.linalg.norm(Q.dequantize_rows(BYTES(q)[3:], BYTES(s)[3:]) - m) <= 2.0 ** -4 * np.linalg.norm(m)
+    x = rows(R, K, 5)
+    M.dsmoe_q8_quantize(handle, R - 3, K, x[3:], qa[3:], sa[3:])
+    eq, es = Q.quantize_rows(NP(x[3:]))
+    np.testing.assert_array_equal(BYTES(qa[3:]), eq)
+    np.testing.assert_array_equal(BYTES(sa[3:]), es)
+
+
 # ----------------------------------------------------------------------- two calls at once
 def test_two_handles_on_two_streams():
     """Products of two handles in flight together give the bits of each alone."""
