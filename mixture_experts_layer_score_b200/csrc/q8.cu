@@ -259,7 +259,9 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512) norm_q8_kernel(const Norm
     t += gridDim.x;
     if (t < a.T) load(t);
     block_sums<1>(ss, red[turn]);
-    const float rstd = rsqrtf(ss[0] / static_cast<float>(d) + a.eps);
+    // rounded to nearest: rsqrtf moves 12% more of u's values across a bf16 border (8192 x 7168:
+    // 490 against 440 of 5.9e7), in the same 88 us
+    const float rstd = __frsqrt_rn(ss[0] / static_cast<float>(d) + a.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
