@@ -648,7 +648,7 @@ class DSMoE:
 
 class DSMoEQ8(DSMoE):
     """The layer with its expert weights in 8 bits. weights: DSMoE's dict; the six expert tensors
-    may be bf16 (quantised here, once; the bf16 tensors are not kept) or (values, scales)
+    may be bf16 (quantised here, once, and waited for; the bf16 tensors are not kept) or (values, scales)
     pairs that already are in 8 bits. sharded.expert_sharded_forward takes it as it takes a
     DSMoE; the token-dispatch form and the backward pass need the bf16 weights."""
 
@@ -669,6 +669,8 @@ class DSMoEQ8(DSMoE):
                 W = (values, scales)
             if W is not None:
                 self.q[name] = tuple(W)
+        if any(n in weights and not isinstance(weights[n], (tuple, list)) for n in Q8_WEIGHTS):
+            torch.cuda.current_stream(device).synchronize()  # the weights are ready for forwards on any stream
         self._weights = DsmoeQ8Weights(*[_ptr(t) for n in Q8_WEIGHTS for t in self.q.get(n, (None, None))])
 
     def alloc_rows(self, T: int):

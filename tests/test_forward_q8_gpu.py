@@ -221,3 +221,24 @@ def test_training_with_a_norm_in_front():
     assert np.linalg.norm(NP(dw) - ew) <= 1e-5 * np.linalg.norm(ew) + 1e-6
     assert M.dsmoe_get_status(layer.handle) == M.DSMOE_OK
     layer.close()
+
+
+def test_weights_are_ready_for_any_stream():
+    """Constructing from bf16 weights waits for their quantisation, queued behind earlier work of
+    the current stream: a forward on another stream follows without an event."""
+    cfg, T = W.get_config("tiny"), 64
+    gpu, _ = make_case(cfg, T)
+    ref = M.DSMoEQ8(M.cfg_from(cfg, T), gpu)
+    want = ref.forward(gpu["x"])["h"]
+    busy = torch.ones(8192, 8192, dtype=torch.bfloat16, device="cuda")
+    out, side = torch.empty_like(busy), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        torch.mm(busy, busy, out=out)
+    layer = M.DSMoEQ8(M.cfg_from(cfg, T), gpu)
+    assert torch.cuda.current_stream().query()
+    o = layer.forward(gpu["x"], stream=side.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(o["h"], want)
+    ref.close()
+    layer.close()
