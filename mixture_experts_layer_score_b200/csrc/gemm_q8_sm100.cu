@@ -7,7 +7,7 @@
 // The scales are powers of two, so the tensor core applies them itself (one e8m0 byte per
 // 32 values of K; a block of 128 uses the same byte for its four MMAs) and the fp32
 // accumulator in tensor memory holds the scaled sum over all of K: no partial sum is ever
-// read back to be rescaled.
+// read back to be rescaled. (A gated product with K > 2560 is summed in chains, see q8_chains.)
 //
 // Orientation as in the bf16 grouped GEMM (gemm_sm100.cu): M = 128 output features per chain,
 // N = the tile's tokens rounded up to 16, two chains sharing the token operand (gated: the
@@ -37,11 +37,12 @@
 //
 // What bounds it: with few rows the weights' bytes (48 experts of 7168 x 2048 and 144 rows: 109 us,
 // 6.3 TB/s); with many the power limit (gate/up, 8192 rows, 32 experts, d = 7168, F = 2048:
-// 250-270 us in a burst, 287-310 repeated at 990 W and 1.2-1.4 GHz, 1.6-1.8 PFLOP/s); with a short K
+// 300 us in a burst, 350-355 repeated, 1.36-1.6 PFLOP/s; 265 and 305 with one chain over K, whose
+// sums are coarser); with a short K
 // loop a tile's start and end (32,768 rows, 64 experts, K = 704, N = 1024: 45 us, floor 21).
 // An MMA of M = 128, K = 32 takes max(64 + 0.14 N, N / 2) cycles, hence the large N.
 // The accumulation over K is the tensor core's: fp32, truncating (relative error 4e-7 at
-// K = 7168).
+// K = 7168, which a bf16 or fp32 output of the plain product carries).
 #include <algorithm>
 
 #include "kernels.h"
@@ -72,6 +73,7 @@ template <int kTok>
 struct Geo {
   static constexpr uint32_t kAccCols = 2 * kTok;
   static constexpr int kBufs = 2 * kAccCols <= kSfCol0 ? 2 : 1;
+  static constexpr int kAccs = kSfCol0 / kAccCols;  // that tensor memory holds
   static constexpr int kStages = kTok > 112 ? 3 : kTok > 32 ? 4 : 5;
   static constexpr uint32_t kXBytes = kTok * kBK;
   static constexpr uint32_t kBoxRows = q8_box_rows(kTok);
@@ -94,6 +96,20 @@ struct Geo {
   static_assert(kXBytes % 1024 == 0 && kTok % kBoxRows == 0 && kBoxRows % 8 == 0,
                 "token boxes start on swizzle atoms");
 };
+
+// The tensor core truncates as it accumulates, so its error grows with the length of the sum: of
+// SwiGLU's values in 8 bits (8192 rows, N = 2048, K = 7168) one chain of MMAs carries 275-332 across
+// an e4m3 border and an fp32 sum 98-119 (K = 2048: 72-81 and 52-60); chains of at most 2048 values,
+// added in fp32, carry 90-146. A gated sum over `quads` groups of four K blocks takes so many chains
+// (up to 2560 values one); chain_end is the K block after chain i's last (kq0, kq1: the CTA's groups,
+// kb1: its end). Their lengths differ by at most one group.
+constexpr int kChainQuads = 4;
+__host__ __device__ __forceinline__ int q8_chains(int quads) {
+  return quads <= kChainQuads + 1 ? 1 : (quads + kChainQuads - 1) / kChainQuads;
+}
+__device__ __forceinline__ int chain_end(int kq0, int kq1, int chains, int i, int kb1) {
+  return min(4 * (kq0 + (i + 1) * (kq1 - kq0) / chains), kb1);
+}
 
 // D[tmem] (+)= (A 2^sfa)(B 2^sfb)^T, e4m3 operands, e8m0 scales in tensor memory.
 __device__ __forceinline__ void mma_q8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -128,6 +144,19 @@ __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t saddr)
   d |= static_cast<uint64_t>(128 >> 4) << 32;  // stride byte offset: next eight rows
   d |= static_cast<uint64_t>(1) << 46;         // descriptor version for sm_100
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// fp32 sums, rounded to nearest.
+__device__ __forceinline__ void add8(uint32_t (&a)[8], const uint32_t (&b)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] = __float_as_uint(__uint_as_float(a[i]) + __uint_as_float(b[i]));
 }
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t c0, int32_t c1,
@@ -267,13 +296,18 @@ __device__ __forceinline__ void add_f32(const Q8GemmArgs& a, int64_t at, float4 
   *reinterpret_cast<float4*>(a.out_f32 + at) = o;
 }
 
-template <int kOut, int kTok, bool kSplit>
+// kLong (gated): K is accumulated in several chains (q8_chains), which the epilogue adds in fp32,
+// rounded to nearest, while the next one runs (160-token tiles have one accumulator: after it).
+template <int kOut, int kTok, bool kSplit, bool kLong>
 __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_constant__ Q8GemmArgs a) {
   using G_ = Geo<kTok>;
   constexpr bool kGated = kOut == kOutGated;
   constexpr int kTileFeat = kGated ? kFeat : 2 * kFeat;  // output features of a tile
   constexpr int kHold = (kTok / kChunk + 1) / 2;         // chunks of an epilogue group
+  constexpr int kRegChunks = kTok > 112 ? 6 : kHold;     // of them (kLong) with their sums in registers
   static_assert(kOut != kOutF32 || G_::kBufs == 2, "the fp32 output leaves the accumulators late");
+  static_assert(!kLong || (kGated && !kSplit), "chains are joined by the epilogue of one CTA");
+  static_assert(!kLong || G_::kBufs * G_::kAccCols + 4 * kChunk * (kHold - kRegChunks) <= kSfCol0, "sums of chains");
   static_assert(!kSplit || (kTok % 8 == 0 && kTok * 2 * kFeat * 4 <= G_::kOffSf), "the ring holds the partial sums");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
@@ -301,6 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
   const int splits = kSplit ? a.splits : 1, rank = kSplit ? static_cast<int>(pair::cta_rank()) : 0;
   const int kq0 = kSplit ? rank * kq_all / splits : 0, kq1 = kSplit ? (rank + 1) * kq_all / splits : kq_all;
   const int kb0 = 4 * kq0, kb1 = kSplit ? min(4 * kq1, kb_all) : kb_all;
+  // chains of this CTA: in a cluster each stays in its accumulator until the join
+  const int chains = kLong ? q8_chains(kq_all) : kSplit && kGated ? min(q8_chains(kq1 - kq0), G_::kAccs) : 1;
   const int tile0 = kSplit ? blockIdx.x / splits : blockIdx.x, tile_step = kSplit ? gridDim.x / splits : gridDim.x;
 
   int32_t* group_begin = reinterpret_cast<int32_t*>(base + G_::kOffRows);
@@ -420,16 +456,33 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
       const Q8Tile t = decode_tile<kTok>(a, tile_start, group_begin, tile);
       const int n_mma = (t.m_valid + 15) & ~15;
       const uint32_t idesc = idesc_q8(kFeat, n_mma, 0);
-      const int acc = it % G_::kBufs;
+      int acc = it % G_::kBufs, chain = 0, first = kb0;
       if (!mbar_wait_converged(&acc_empty[acc], ((it / G_::kBufs) & 1) ^ 1u, a.wait_limit_ns, abort_flag)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const uint32_t d0 = tmem_base + acc * G_::kAccCols;
+      uint32_t d0 = tmem_base + acc * G_::kAccCols;
+      int last = kLong || kSplit ? chain_end(kq0, kq1, chains, 0, kb1) - 1 : kb1 - 1;  // of this chain
       uint32_t sf = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
         const uint32_t id = kb & 3;
+        if ((kLong || kSplit) && kb > last) {  // the next chain
+          first = kb;
+          last = chain_end(kq0, kq1, chains, ++chain, kb1) - 1;
+          if (kLong) {
+            ++it;
+            acc = it % G_::kBufs;
+            if (!mbar_wait_converged(&acc_empty[acc], ((it / G_::kBufs) & 1) ^ 1u, a.wait_limit_ns, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            d0 = tmem_base + acc * G_::kAccCols;
+          } else {
+            d0 += G_::kAccCols;
+          }
+        }
         if (id == 0) {
           // the columns of this set were last read by the MMAs of two groups ago
           const uint32_t slot = quad % kSfSlots;
@@ -463,13 +516,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
 #pragma unroll
           for (int k = 0; k < kBK / kMmaK; ++k) {
             const uint64_t dk = static_cast<uint64_t>(2 * k);
-            const uint32_t accum = (kb > kb0 || k) ? 1u : 0u;
+            const uint32_t accum = (kb > first || k) ? 1u : 0u;
             mma_q8_ss(d0, w0 + dk, xd + dk, di, sf, sf + 8, accum);
             mma_q8_ss(d0 + kTok, w1 + dk, xd + dk, di, kGated ? sf + 4 : sf, sf + 8, accum);
           }
           mma_commit(&empty[stage]);
           if (id == 3 || kb == kb1 - 1) mma_commit(&sf_empty[quad % kSfSlots]);
-          if (kb == kb1 - 1) mma_commit(&acc_full[acc]);
+          if (kb == (kLong ? last : kb1 - 1)) mma_commit(&acc_full[acc]);
         }
         __syncwarp();
         if (id == 3 || kb == kb1 - 1) ++quad;
@@ -542,8 +595,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
     uint32_t buf = 0;  // staging buffer of the next chunk
     const int w4 = (warp - 2) & 3;  // this warp's rows of a staged chunk: 4 w4 .. 4 w4 + 3
     int it = 0;
-    for (int tile = tile0; tile < total; tile += tile_step, ++it) {
-      const Q8Tile t = decode_tile<kTok>(a, tile_start, group_begin, tile);
+    // the accumulator of turn `it` is complete: the same answer for the whole group (its warps are
+    // at most one turn apart)
+    auto filled = [&]() -> bool {
       const int acc = it % G_::kBufs;
       if (leader) {
         const bool ok = mbar_wait_checked(&acc_full[acc], (it / G_::kBufs) & 1, a.wait_limit_ns, abort_flag);
@@ -554,10 +608,15 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
         }
       }
       group_sync(half);
-      // the same answer for the whole group (its warps are at most one tile apart)
-      if (!group_ok[2 * half + (it & 1)]) break;
+      if (!group_ok[2 * half + (it & 1)]) return false;
       (void)mbar_try_wait(&acc_full[acc], (it / G_::kBufs) & 1);
       tc_fence_after();
+      return true;
+    };
+    for (int tile = tile0; tile < total; tile += tile_step, ++it) {
+      const Q8Tile t = decode_tile<kTok>(a, tile_start, group_begin, tile);
+      if (!filled()) break;
+      const int acc = it % G_::kBufs;
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * G_::kAccCols;
       const int n_chunks = (t.m_valid + kChunk - 1) / kChunk;
       const int n0 = t.n_blk * kTileFeat;
@@ -599,28 +658,90 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
         // First the accumulators move to registers (gated: through SwiGLU; plain: both chains
         // rounded into one register), so that the next tile's MMAs may overwrite them ...
         uint32_t hold[kHold][kChunk], v0[2][kChunk], v1[2][kChunk];
+        if constexpr (kLong) {
+          // ... with the sums of the chains before the last: those of the group's first kRegChunks
+          // chunks in registers, of the others in the columns that the accumulators leave
+          uint32_t u[kRegChunks][kChunk];
 #pragma unroll
-        for (int i = 0; i < kHold; i += 2) {  // two chunks at a time
-          if (2 * i + half >= n_chunks) break;
-          const uint32_t at = tb + kChunk * (2 * i + half);
-          tmem_ld8(at, v0[0]);
-          tmem_ld8(at + kTok, v1[0]);
-          if (i + 1 < kHold) {  // (columns past the tile's tokens hold what nothing reads)
-            tmem_ld8(at + 2 * kChunk, v0[1]);
-            tmem_ld8(at + 2 * kChunk + kTok, v1[1]);
+          for (int i = 0; i < kRegChunks; ++i)
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j) hold[i][j] = u[i][j] = 0;
+          const uint32_t spare = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + G_::kBufs * G_::kAccCols +
+                                 half * (kHold - kRegChunks) * 2 * kChunk;
+          uint32_t from = tb;
+          bool ok = true;
+#pragma unroll 1
+          for (int chain = 0; chain + 1 < chains; ++chain) {
+#pragma unroll
+            for (int i = 0; i < kHold; ++i) {
+              if (2 * i + half >= n_chunks) break;
+              const uint32_t at = from + kChunk * (2 * i + half), kept = spare + (i - kRegChunks) * 2 * kChunk;
+              if (i < kRegChunks) {
+                tmem_ld8(at, v0[0]);
+                tmem_ld8(at + kTok, v1[0]);
+                tmem_wait_ld();
+                add8(hold[i], v0[0]);
+                add8(u[i < kRegChunks ? i : 0], v1[0]);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  tmem_ld8(at + k * kTok, v0[0]);
+                  if (chain > 0) tmem_ld8(kept + k * kChunk, v1[0]);
+                  tmem_wait_ld();
+                  if (chain > 0) add8(v0[0], v1[0]);
+                  tmem_st8(kept + k * kChunk, v0[0]);
+                }
+              }
+            }
+            if (kHold > kRegChunks) tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[it % G_::kBufs]);
+            ++it;
+            ok = filled();
+            if (!ok) break;
+            from = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + it % G_::kBufs * G_::kAccCols;
           }
-          tmem_wait_ld();
+          if (!ok) break;
 #pragma unroll
-          for (int j = 0; j < 2 * kChunk; ++j) {
-            const int s = j >= kChunk ? 1 : 0;
-            if (i + s >= kHold) break;
-            const float x = __uint_as_float(v0[s][j & 7]), y = __uint_as_float(v1[s][j & 7]);
-            hold[i + s][j & 7] = kGated ? __float_as_uint(swiglu(x, y)) : pack_bf16x2(x, y);
+          for (int i = 0; i < kHold; ++i) {
+            if (2 * i + half >= n_chunks) break;
+            const uint32_t at = from + kChunk * (2 * i + half), kept = spare + (i - kRegChunks) * 2 * kChunk;
+            tmem_ld8(at, v0[0]);
+            if (i >= kRegChunks) tmem_ld8(kept, hold[i]);
+            tmem_ld8(at + kTok, v1[0]);
+            if (i >= kRegChunks) tmem_ld8(kept + kChunk, u[0]);
+            tmem_wait_ld();
+            add8(hold[i], v0[0]);
+            add8(v1[0], u[i < kRegChunks ? i : 0]);
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j)
+              hold[i][j] = __float_as_uint(swiglu(__uint_as_float(hold[i][j]), __uint_as_float(v1[0][j])));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kHold; i += 2) {  // two chunks at a time
+            if (2 * i + half >= n_chunks) break;
+            const uint32_t at = tb + kChunk * (2 * i + half);
+            tmem_ld8(at, v0[0]);
+            tmem_ld8(at + kTok, v1[0]);
+            if (i + 1 < kHold) {  // (columns past the tile's tokens hold what nothing reads)
+              tmem_ld8(at + 2 * kChunk, v0[1]);
+              tmem_ld8(at + 2 * kChunk + kTok, v1[1]);
+            }
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 2 * kChunk; ++j) {
+              const int s = j >= kChunk ? 1 : 0;
+              if (i + s >= kHold) break;
+              const float x = __uint_as_float(v0[s][j & 7]), y = __uint_as_float(v1[s][j & 7]);
+              hold[i + s][j & 7] = kGated ? __float_as_uint(swiglu(x, y)) : pack_bf16x2(x, y);
+            }
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[acc]);
+        if (lane == 0) mbar_arrive(&acc_empty[it % G_::kBufs]);
         if constexpr (!kGated) {
           // ... then they are stored: a thread's two are neighbours in the output row, and a
           // warp's words of a token make one line
@@ -697,6 +818,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
         tmem_ld8(tb + kChunk * c, p0);
         tmem_ld8(tb + kTok + kChunk * c, p1);
         tmem_wait_ld();
+        for (int chain = 1; chain < chains; ++chain) {
+          uint32_t v0[kChunk], v1[kChunk];
+          tmem_ld8(tb + chain * G_::kAccCols + kChunk * c, v0);
+          tmem_ld8(tb + chain * G_::kAccCols + kTok + kChunk * c, v1);
+          tmem_wait_ld();
+          add8(p0, v0);
+          add8(p1, v1);
+        }
 #pragma unroll
         for (int j = 0; j < kChunk; ++j) {
           const int tok = kChunk * c + j;
@@ -751,13 +880,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
   }
 }
 
-template <int kOut, int kTok, bool kSplit>
+template <int kOut, int kTok, bool kSplit, bool kLong>
 cudaError_t launch_one(const Q8GemmArgs& a, int grid, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(gemm_q8_kernel<kOut, kTok, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(gemm_q8_kernel<kOut, kTok, kSplit, kLong>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(Geo<kTok>::kSmemBytes));
   if (e != cudaSuccess) return e;
   if (!kSplit) {
-    gemm_q8_kernel<kOut, kTok, kSplit><<<grid, kThreads, Geo<kTok>::kSmemBytes, s>>>(a);
+    gemm_q8_kernel<kOut, kTok, kSplit, kLong><<<grid, kThreads, Geo<kTok>::kSmemBytes, s>>>(a);
     return cudaGetLastError();
   }
   cudaLaunchAttribute cluster;
@@ -772,16 +901,22 @@ cudaError_t launch_one(const Q8GemmArgs& a, int grid, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = &cluster;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gemm_q8_kernel<kOut, kTok, kSplit>, a);
+  return cudaLaunchKernelEx(&cfg, gemm_q8_kernel<kOut, kTok, kSplit, kLong>, a);
 }
 
 template <int kOut>
 cudaError_t launch_tok(const Q8GemmArgs& a, int tok, int grid, cudaStream_t s) {
-  if (a.splits > 1) return tok == 32 ? launch_one<kOut, 32, true>(a, grid, s) : launch_one<kOut, 112, true>(a, grid, s);
-  if (tok == 32) return launch_one<kOut, 32, false>(a, grid, s);
+  if (a.splits > 1)
+    return tok == 32 ? launch_one<kOut, 32, true, false>(a, grid, s) : launch_one<kOut, 112, true, false>(a, grid, s);
+  if constexpr (kOut == kOutGated)
+    if (q8_chains((a.K + 511) / 512) > 1)
+      return tok == 32    ? launch_one<kOut, 32, false, true>(a, grid, s)
+             : tok == 112 ? launch_one<kOut, 112, false, true>(a, grid, s)
+                          : launch_one<kOut, 160, false, true>(a, grid, s);
+  if (tok == 32) return launch_one<kOut, 32, false, false>(a, grid, s);
   if constexpr (kOut != kOutF32)
-    if (tok == 240) return launch_one<kOut, 240, false>(a, grid, s);
-  return launch_one<kOut, 112, false>(a, grid, s);
+    if (tok == 240) return launch_one<kOut, 240, false, false>(a, grid, s);
+  return launch_one<kOut, 112, false, false>(a, grid, s);
 }
 
 // Tiles of `tok` rows that R rows in E groups make at most.
@@ -795,28 +930,32 @@ int64_t token_tiles(int64_t R, int E, int tok) { return (R + (tok - 1) * std::mi
 //        56 rows, N = 128, K = 256, gated: 8.3 against 10.5).
 //   240  one accumulator, so that the start of a tile's epilogue is exposed, but an MMA at
 //        N = 240 costs 0.5 cycles a token and at N = 112 0.75: from g = 100 on where the K loop is
-//        long enough to bury that start. Gated, K >= 1024 (K = 1024, g = 512: 87 against 99;
+//        long enough to bury that start. Gated, 1024 <= K <= 2560 (K = 1024, g = 512: 87 against 99;
 //        K = 2048, g = 120: 62.8 against 67.5; K = 704, g = 300: 61 against 57 the other way).
 //        Plain, whose 112-token tiles run two accumulators over a cheaper epilogue, K >= 4096
 //        (K = 7168, g = 100: 98.8 against 107), or g >= 240 with g K >= 350,000 (K = 1280,
 //        g = 512: 53.8 against 61.1; K = 2048, g = 200: 45.4 against 43.3 and K = 448, g = 512:
 //        35.2 against 33.4 the other way).
+//   160  gated, K > 2560, from g = 110 on: the sums of two chains and more have to be kept, and those
+//        of 240 tokens have no place in registers and tensor memory (of 160: 6 of a group's 10 chunks
+//        in registers). K = 7168, g = 120: 187 against 223 with 112, g = 256: 315 against 343, g = 100:
+//        176 against 166 the other way.
 //   112  the rest, and in place of 32 where its clusters (q8_splits) shorten a CTA's K loop by 14
 //        blocks or more (128 rows, gated, K = 7168: 18.7 against 22.3; 256 rows: 26.9 against 30.5;
 //        4 groups of 169 rows, N = 600, K = 3968: 16.6 against 18.7; 13 blocks, 5 groups of 184 rows,
 //        K = 3280, gated: 21.7 against 18.6 the other way).
-static int q8_splits(int64_t tiles, int tok, int K, int num_sms);
+static int q8_splits(int64_t tiles, int tok, int K, bool gated, int num_sms);
 int q8_token_tile(int64_t R, int E, int N, int K, bool gated, int num_sms) {
   const int64_t n_tiles = gated ? (N + 127) / 128 : (N + 255) / 256, g = R / E;
   if (g <= 16) return 32;
   if (std::max<int64_t>(E, (R + 31) / 32) * n_tiles <= num_sms) {
     const int kb = (K + kBK - 1) / kBK;
-    const int s32 = q8_splits(token_tiles(R, E, 32) * n_tiles, 32, K, num_sms);
-    const int s112 = q8_splits(token_tiles(R, E, 112) * n_tiles, 112, K, num_sms);
+    const int s32 = q8_splits(token_tiles(R, E, 32) * n_tiles, 32, K, gated, num_sms);
+    const int s112 = q8_splits(token_tiles(R, E, 112) * n_tiles, 112, K, gated, num_sms);
     return kb / s32 - kb / s112 >= 14 ? 112 : 32;
   }
-  const bool large = gated ? g >= 100 && K >= 1024
-                           : (g >= 100 && K >= 4096) || (g >= 240 && g * K >= 350000);
+  if (gated && q8_chains((K + 511) / 512) > 1) return g >= 110 ? 160 : 112;
+  const bool large = gated ? g >= 100 && K >= 1024 : (g >= 100 && K >= 4096) || (g >= 240 && g * K >= 350000);
   return large ? 240 : 112;
 }
 
@@ -824,13 +963,15 @@ int q8_token_tile(int64_t R, int E, int N, int K, bool gated, int num_sms) {
 // 15 clusters of 8 CTAs, 33 of 4, 74 of 2) and that leave each CTA a group of four K blocks.
 // One row, N = 128, K = 7168, gated: 28.4 us alone, 18.7, 14.0 and 10.5 with 2, 4 and 8; 16 tiles:
 // 28.9, 18.7, 14.6 and 18.8 (the 16th cluster of 8 runs afterwards). Joining the sums of a
-// 112-token tile takes longer, so there the K loop has to get 14 blocks shorter.
-static int q8_splits(int64_t tiles, int tok, int K, int num_sms) {
+// 112-token tile takes longer, so there the K loop has to get 14 blocks shorter; two chains of a gated
+// sum are what tensor memory holds of it (of 32 tokens seven, which any K can do with).
+static int q8_splits(int64_t tiles, int tok, int K, bool gated, int num_sms) {
   const int groups = (K + 511) / 512, kb = (K + kBK - 1) / kBK;
   if (tok > 112) return 1;
   for (int s = 8; s > 1; s >>= 1) {
     const int idle = s == 8 ? 28 : s == 4 ? 16 : 0;
-    if (tiles * s <= num_sms - idle && groups >= s) return tok == 32 || kb - kb / s >= 14 ? s : 1;
+    if (tiles * s <= num_sms - idle && groups >= s)
+      return tok == 32 || (kb - kb / s >= 14 && (!gated || q8_chains((groups + s - 1) / s) <= 2)) ? s : 1;
   }
   return 1;
 }
@@ -840,7 +981,7 @@ cudaError_t launch_gemm_q8(const Q8GemmArgs& args, int tok, int num_sms, cudaStr
   const bool gated = a.q_out != nullptr;
   const int64_t n_tiles = (a.N + (gated ? 127 : 255)) / (gated ? 128 : 256);
   const int64_t bound = token_tiles(a.R, a.E, tok) * n_tiles;
-  a.splits = q8_splits(bound, tok, a.K, num_sms);
+  a.splits = q8_splits(bound, tok, a.K, gated, num_sms);
   const int grid = static_cast<int>(a.splits > 1 ? bound * a.splits : std::min<int64_t>(bound, num_sms));
   if (gated) return launch_tok<kOutGated>(a, tok, grid, s);
   return a.out_f32 ? launch_tok<kOutF32>(a, tok, grid, s) : launch_tok<kOutBf16>(a, tok, grid, s);

@@ -368,7 +368,7 @@ struct Q8GemmArgs {
 // Tokens per tile for R rows over E groups, and the row box of map_a: a tile copies the
 // boxes that hold its rows. (The fp32 output takes tiles of at most 112.)
 int q8_token_tile(int64_t R, int E, int N, int K, bool gated, int num_sms);
-constexpr int q8_box_rows(int tok) { return tok == 240 ? 48 : tok == 112 ? 56 : 16; }
+constexpr int q8_box_rows(int tok) { return tok == 240 ? 48 : tok == 160 ? 32 : tok == 112 ? 56 : 16; }
 cudaError_t launch_gemm_q8(const Q8GemmArgs& a, int tok, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- errors (dsmoe_api.cu)
