@@ -583,6 +583,27 @@ def workspace_view(handle, name: str, device: int = 0):
     return t.view(rows, cols)
 
 
+def _empty(stream, device: int, shapes):
+    """Tensors for work on `stream` (None: the current one), as [(shape, dtype), ...]. torch reuses freed
+    memory in the order of the stream it was allocated on, so they are allocated on `stream`: a
+    block whose last use there or elsewhere is still to come is not taken. The current stream is
+    recorded as their user, so that what it still reads of them is not overwritten once they are freed."""
+    import torch
+    dev = torch.device("cuda", device)
+    if not _DTYPES:
+        _setup()
+    raw, here = None if stream is None else _stream(stream), _raw_stream(device)
+    if raw is None or raw == here:
+        return [torch.empty(shape, dtype=dtype, device=dev) for shape, dtype in shapes]
+    on = torch.cuda.ExternalStream(raw, device=dev) if raw else torch.cuda.default_stream(dev)
+    current = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(on):
+        out = [torch.empty(shape, dtype=dtype, device=dev) for shape, dtype in shapes]
+    for t in out:
+        t.record_stream(current)
+    return out
+
+
 class DSMoE:
     """A handle plus the weight tensors of one layer; forward() allocates the outputs with
     torch (device memory only) and calls dsmoe_forward."""
@@ -620,25 +641,22 @@ class DSMoE:
         except Exception:
             pass
 
-    def alloc_outputs(self, T: int, with_scores: bool = False):
+    def alloc_outputs(self, T: int, with_scores: bool = False, stream=None):
+        """forward()'s outputs for T tokens, for use on `stream` (None: the current one)."""
         import torch
-        dev = torch.device("cuda", self.device)
-        c = self.cfg
-        h_dtype = torch.float32 if self.range_flags & DSMOE_RANGE_PARTIAL else torch.bfloat16
-        out = dict(h=torch.empty((T, c.d_model), dtype=h_dtype, device=dev),
-                   topk_idx=torch.empty((T, self.k_active), dtype=torch.int32, device=dev),
-                   gates=torch.empty((T, self.k_active), dtype=torch.float32, device=dev),
-                   counts=torch.empty((c.n_routed,), dtype=torch.int32, device=dev),
-                   f=torch.empty((c.n_routed,), dtype=torch.float32, device=dev),
-                   P=torch.empty((c.n_routed,), dtype=torch.float32, device=dev),
-                   P_sum=torch.empty((c.n_routed,), dtype=torch.float32, device=dev))
-        out["scores"] = (torch.empty((T, c.n_routed), dtype=torch.float32, device=dev)
-                         if with_scores and c.score != DSMOE_ROUTE_HASH else None)
+        c, f32, i32 = self.cfg, torch.float32, torch.int32
+        N, K = (c.n_routed,), (T, self.k_active)
+        shapes = dict(h=((T, c.d_model), f32 if self.range_flags & DSMOE_RANGE_PARTIAL else torch.bfloat16),
+                      topk_idx=(K, i32), gates=(K, f32), counts=(N, i32), f=(N, f32), P=(N, f32), P_sum=(N, f32))
+        if with_scores and c.score != DSMOE_ROUTE_HASH:
+            shapes["scores"] = ((T, c.n_routed), f32)
+        out = dict(zip(shapes, _empty(stream, self.device, shapes.values())))
+        out.setdefault("scores", None)
         return out
 
     def forward(self, x, token_ids=None, out=None, with_scores: bool = False, stream=None):
         T = x.shape[0]
-        o = self.alloc_outputs(T, with_scores) if out is None else out
+        o = self.alloc_outputs(T, with_scores, stream) if out is None else out
         w = self.w
         dsmoe_forward(self.handle, T, x, token_ids, w.get("W_router"), w.get("b"), w["W_gate"], w["W_up"],
                       w["W_down"], w.get("Ws_gate"), w.get("Ws_up"), w.get("Ws_down"), o["h"], o["topk_idx"],
@@ -673,21 +691,24 @@ class DSMoEQ8(DSMoE):
             torch.cuda.current_stream(device).synchronize()  # the weights are ready for forwards on any stream
         self._weights = DsmoeQ8Weights(*[_ptr(t) for n in Q8_WEIGHTS for t in self.q.get(n, (None, None))])
 
-    def alloc_rows(self, T: int):
-        """Buffers of T 8-bit rows: values [T, d], scales [T, S(d)]."""
+    def alloc_rows(self, T: int, stream=None):
+        """Buffers of T 8-bit rows, values [T, d] and scales [T, S(d)], for use on `stream`."""
         import torch
-        dev, d = torch.device("cuda", self.device), self.cfg.d_model
-        return (torch.empty((T, d), dtype=torch.float8_e4m3fn, device=dev),
-                torch.empty((T, dsmoe_q8_scale_cols(d)), dtype=torch.float8_e8m0fnu, device=dev))
+        d = self.cfg.d_model
+        return tuple(_empty(stream, self.device, [((T, d), torch.float8_e4m3fn),
+                                                  ((T, dsmoe_q8_scale_cols(d)), torch.float8_e8m0fnu)]))
 
     def forward(self, x, token_ids=None, out=None, with_scores: bool = False, stream=None, residual=None, x_q=None):
-        """The layer on x; x_q: its 8-bit rows (values, scales) where the caller has them (else they
-        are made here and returned as "x_q", so that they live as long as the outputs, whatever
-        the stream); residual: what the layer's output is added to in place of x."""
+        """The layer on x; x_q: its 8-bit rows (values, scales) where the caller has them, else they are
+        made here and returned as "x_q", which lives as long as the outputs; an `out` that holds it
+        from an earlier call with as many tokens has it overwritten like the other outputs.
+        residual: what the layer's output is added to in place of x."""
         T = x.shape[0]
-        o = self.alloc_outputs(T, with_scores) if out is None else out
+        o = self.alloc_outputs(T, with_scores, stream) if out is None else out
         if x_q is None:
-            x_q = o["x_q"] = self.alloc_rows(T)
+            x_q = o.get("x_q")
+            if x_q is None or x_q[0].shape[0] != T:
+                x_q = o["x_q"] = self.alloc_rows(T, stream)
             dsmoe_q8_quantize(self.handle, T, self.cfg.d_model, x, *x_q, stream)
         w = self.w
         dsmoe_forward_q8(self.handle, T, x, *x_q, residual, token_ids, w.get("W_router"), w.get("b"), self._weights,
@@ -700,7 +721,8 @@ class DSMoEQ8(DSMoE):
         layer's outputs and "r", "u", "x_q" (the 8-bit rows of u)."""
         import torch
         T = x.shape[0]
-        r, u, x_q = torch.empty_like(x), torch.empty_like(x), self.alloc_rows(T)
+        r, u = _empty(stream, self.device, [(x.shape, torch.bfloat16)] * 2)
+        x_q = self.alloc_rows(T, stream)
         dsmoe_norm_q8(self.handle, T, x, residual, w, eps, r, u, *x_q, stream)
         o = self.forward(u, token_ids, None, with_scores, stream, r, x_q)
         o["r"], o["u"], o["x_q"] = r, u, x_q
