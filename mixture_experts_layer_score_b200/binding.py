@@ -197,13 +197,22 @@ def dsmoe_workspace_bytes(cfg: DsmoeCfg) -> int:
     return n.value
 
 
-_handles: Dict[int, tuple] = {}  # live handles: (device, d_model)
+class _Live:
+    """What a handle was made and set up with: the checks of tensors against it need no call."""
+    __slots__ = ("device", "cfg", "experts", "k", "flags")
+
+    def __init__(self, device: int, cfg: DsmoeCfg):
+        self.device, self.cfg = device, DsmoeCfg.from_buffer_copy(cfg)
+        self.experts, self.k, self.flags = cfg.n_routed, cfg.top_k, DSMOE_RANGE_ADD_SHARED
+
+
+_handles: Dict[int, _Live] = {}
 
 
 def dsmoe_create(cfg: DsmoeCfg, device: int = 0) -> int:
     h = ctypes.c_void_p()
     _check(_lib.dsmoe_create(ctypes.byref(cfg), int(device), ctypes.byref(h)), "dsmoe_create")
-    _handles[h.value] = (int(device), cfg.d_model)
+    _handles[h.value] = _Live(int(device), cfg)
     return h.value
 
 
@@ -269,6 +278,8 @@ def dsmoe_get_gemm_kernel(handle) -> int:
 
 def dsmoe_set_selection(handle, mask_top: int, k_active: int) -> None:
     _check(_lib.dsmoe_set_selection(handle, int(mask_top), int(k_active)), "dsmoe_set_selection")
+    if handle in _handles:
+        _handles[handle].k = int(k_active)
 
 
 def dsmoe_get_selection(handle):
@@ -279,6 +290,8 @@ def dsmoe_get_selection(handle):
 
 def dsmoe_set_expert_range(handle, e_begin: int, e_end: int, flags: int) -> None:
     _check(_lib.dsmoe_set_expert_range(handle, int(e_begin), int(e_end), int(flags)), "dsmoe_set_expert_range")
+    if handle in _handles:
+        _handles[handle].experts, _handles[handle].flags = int(e_end) - int(e_begin), int(flags)
 
 
 def dsmoe_get_expert_range(handle):
@@ -427,7 +440,7 @@ def _take(where: str, handle, stream, *tensors):
     the handle's device."""
     if not _DTYPES:
         _setup()
-    device = _handles[handle][0] if handle in _handles else None
+    device = _handles[handle].device if handle in _handles else None
     ptrs = []
     for name, t, kind, n in tensors:
         if t is not None and t.__class__ is not int:
@@ -441,10 +454,23 @@ def _take(where: str, handle, stream, *tensors):
     return ptrs, _stream(stream)
 
 
-def _refuse(where: str, name: str, t, kind: str, n: int):
+def _take_outputs(where: str, live, *tensors):
+    """As _take, for outputs, which may be longer than the call needs."""
+    ptrs = []
+    for name, t, kind, n in tensors:
+        if t is not None and t.__class__ is not int:
+            if live is not None and (t.dtype not in _DTYPES[kind] or t.numel() < n or not t.is_contiguous() or
+                                     t.get_device() != live.device):
+                _refuse(where, name, t, kind, n, least=True)
+            t = t.data_ptr()
+        ptrs.append(t)
+    return ptrs
+
+
+def _refuse(where: str, name: str, t, kind: str, n: int, least: bool = False):
     if t.dtype not in _DTYPES[kind]:
         why = f"is {t.dtype}, not {' or '.join(map(str, _DTYPES[kind]))}"
-    elif t.numel() != n:
+    elif t.numel() < n or (t.numel() != n and not least):
         why = f"has {t.numel()} elements, not {n}"
     elif not t.is_contiguous():
         why = "is not contiguous"
@@ -458,9 +484,10 @@ def _norm_width(where, handle, w) -> int:
     known = _handles.get(handle)
     if known is None:
         return w.numel() if hasattr(w, "numel") else 0
-    if w is not None and w.__class__ is not int and w.numel() != known[1]:
-        raise DsmoeError(DSMOE_ERR_INVALID_ARG, where, f"w has {w.numel()} elements, not d_model = {known[1]}")
-    return known[1]
+    d = known.cfg.d_model
+    if w is not None and w.__class__ is not int and w.numel() != d:
+        raise DsmoeError(DSMOE_ERR_INVALID_ARG, where, f"w has {w.numel()} elements, not d_model = {d}")
+    return d
 
 
 def dsmoe_q8_scale_cols(C: int) -> int:
@@ -530,22 +557,48 @@ def dsmoe_q8_gated_matmul(handle, E, R, N, K, offsets, a, a_scales, W_gate, gate
     _check(_lib.dsmoe_q8_gated_matmul(handle, E, R, N, K, *p, s), where)
 
 
+def _q8_weight_shapes(cfg: DsmoeCfg):
+    """(experts, N, K) of each expert tensor by name; experts None: as many as the handle applies."""
+    d, F, Fs, Ks = cfg.d_model, cfg.d_ff, cfg.d_ff_shared, cfg.n_shared
+    return {"W_gate": (None, F, d), "W_up": (None, F, d), "W_down": (None, d, F),
+            "Ws_gate": (Ks, Fs, d), "Ws_up": (Ks, Fs, d), "Ws_down": (Ks, d, Fs)}
+
+
+def _take_q8_weights(where: str, handle, weights: Dict, experts: int) -> DsmoeQ8Weights:
+    """The struct of 8-bit weights given as (values, scales) pairs by name, each checked against
+    the handle's configuration and the number of routed experts."""
+    ptrs = []
+    for name, (E, N, K) in _q8_weight_shapes(_handles[handle].cfg).items():
+        E = experts if E is None else E
+        values, scales = (E and weights.get(name)) or (None, None)
+        for what, t, rows, cols in (("values", values, N, K), ("scales", scales, -(-N // 128), _scale_cols(K))):
+            if getattr(t, "ndim", 0) == 3 and tuple(t.shape) != (E, rows, cols):
+                raise DsmoeError(DSMOE_ERR_INVALID_ARG, where,
+                                 f"{name} {what} are {tuple(t.shape)}, not {(E, rows, cols)}")
+            ptrs += _take(where, handle, 0, (f"{name} {what}", t, "q8", E * rows * cols))[0]
+    return DsmoeQ8Weights(*ptrs)
+
+
 def dsmoe_forward_q8(handle, T, x, x_q, x_scales, residual, token_ids, W_router, b, weights, h, topk_idx, gates,
                      counts, f, P, P_sum=None, scores_dbg=None, stream=None) -> None:
-    """weights: a DsmoeQ8Weights, or a dict of (values, scales) tensor pairs by name (Q8_WEIGHTS)."""
+    """weights: a dict of (values, scales) tensor pairs by name (Q8_WEIGHTS), or a DsmoeQ8Weights, whose
+    addresses are taken as they are. Outputs may be longer than T tokens need."""
     where, T = "dsmoe_forward_q8", int(T)
+    live = _handles.get(handle)
     if not isinstance(weights, DsmoeQ8Weights):
-        pairs = {n: weights.get(n) or (None, None) for n in Q8_WEIGHTS}
-        weights = DsmoeQ8Weights(*[_ptr(t) for n in Q8_WEIGHTS for t in pairs[n]])
-    d = _handles[handle][1] if handle in _handles else 0
+        weights = DsmoeQ8Weights() if live is None else _take_q8_weights(where, handle, weights, live.experts)
+    d, N, k = (live.cfg.d_model, live.cfg.n_routed, live.k) if live is not None else (0, 0, 0)
     n = T * d
-    rows = (("x", x, "bf16", n), ("x_q", x_q, "q8", n), ("x_scales", x_scales, "q8", T * _scale_cols(d)),
-            ("residual", residual, "bf16", n))
-    (x, x_q, x_scales, residual), s = _take(where, handle, stream, *rows)
-    st = _lib.dsmoe_forward_q8(handle, T, x, x_q, x_scales, residual, _ptr(token_ids), _ptr(W_router), _ptr(b),
-                               ctypes.byref(weights), *[_ptr(t) for t in (
-                                   h, topk_idx, gates, counts, f, P, P_sum, scores_dbg)], s)
-    _check(st, where)
+    (x, x_q, x_scales, residual, token_ids, W_router, b), s = _take(
+        where, handle, stream, ("x", x, "bf16", n), ("x_q", x_q, "q8", n),
+        ("x_scales", x_scales, "q8", T * _scale_cols(d)), ("residual", residual, "bf16", n),
+        ("token_ids", token_ids, "i32", T), ("W_router", W_router, "bf16", N * d), ("b", b, "f32", N))
+    outs = _take_outputs(
+        where, live, ("h", h, "f32" if live is not None and live.flags & DSMOE_RANGE_PARTIAL else "bf16", n),
+        ("topk_idx", topk_idx, "i32", T * k), ("gates", gates, "f32", T * k), ("counts", counts, "i32", N),
+        ("f", f, "f32", N), ("P", P, "f32", N), ("P_sum", P_sum, "f32", N), ("scores_dbg", scores_dbg, "f32", T * N))
+    _check(_lib.dsmoe_forward_q8(handle, T, x, x_q, x_scales, residual, token_ids, W_router, b, ctypes.byref(weights),
+                                 *outs, s), where)
 
 
 _WS_DTYPES = {"logits": "float32", "offsets": "int32", "slot_of": "int32", "Xp": "bfloat16",
@@ -667,29 +720,46 @@ class DSMoE:
 class DSMoEQ8(DSMoE):
     """The layer with its expert weights in 8 bits. weights: DSMoE's dict; the six expert tensors
     may be bf16 (quantised here, once, and waited for; the bf16 tensors are not kept) or (values, scales)
-    pairs that already are in 8 bits. sharded.expert_sharded_forward takes it as it takes a
+    pairs that already are in 8 bits, with scales of dsmoe_q8_scale_cols bytes a row; they are checked
+    here against cfg, and their number of experts against the expert range in force at a forward. sharded.expert_sharded_forward takes it as it takes a
     DSMoE; the token-dispatch form and the backward pass need the bf16 weights."""
 
     def __init__(self, cfg: DsmoeCfg, weights: Dict, device: int = 0):
         import torch
         super().__init__(cfg, {k: v for k, v in weights.items() if k not in Q8_WEIGHTS}, device)
-        self.q = {}
+        where, shapes = "DSMoEQ8", _q8_weight_shapes(cfg)
+        self.q, self.experts = {}, None
         for name in Q8_WEIGHTS:
-            W = weights.get(name)
-            if W is not None and not isinstance(W, (tuple, list)):
-                E, N, K = W.shape
-                if E == 0:
-                    continue
+            W, (E, N, K) = weights.get(name), shapes[name]
+            if W is None or E == 0:  # (a configuration without shared experts reads none)
+                continue
+            pair = isinstance(W, (tuple, list))
+            values = W[0] if pair else W
+            if hasattr(values, "numel"):  # (raw addresses are taken as they are)
+                if E is None:
+                    E = values.numel() // (N * K) if self.experts is None else self.experts
+                    self.experts = E
+                if not pair and tuple(W.shape) != (E, N, K):
+                    raise DsmoeError(DSMOE_ERR_INVALID_ARG, where, f"{name} is {tuple(W.shape)}, not {(E, N, K)}")
+            if not pair:
                 values = torch.empty((E, N, K), dtype=torch.float8_e4m3fn, device=W.device)
                 scales = torch.empty((E, -(-N // 128), dsmoe_q8_scale_cols(K)), dtype=torch.float8_e8m0fnu,
                                      device=W.device)
                 dsmoe_q8_quantize_weights(self.handle, E, N, K, W, values, scales)
                 W = (values, scales)
-            if W is not None:
-                self.q[name] = tuple(W)
+            self.q[name] = tuple(W)
         if any(n in weights and not isinstance(weights[n], (tuple, list)) for n in Q8_WEIGHTS):
             torch.cuda.current_stream(device).synchronize()  # the weights are ready for forwards on any stream
-        self._weights = DsmoeQ8Weights(*[_ptr(t) for n in Q8_WEIGHTS for t in self.q.get(n, (None, None))])
+        self._weights = _take_q8_weights(where, self.handle, self.q, self.experts or 0)
+
+    def _check_experts(self, experts: int):
+        if self.experts is not None and self.experts != experts:
+            raise DsmoeError(DSMOE_ERR_INVALID_ARG, "DSMoEQ8", f"the weights hold {self.experts} routed experts, not "
+                             f"the {experts} of the expert range")
+
+    def set_expert_range(self, e_begin: int, e_end: int, partial: bool = True, add_shared: bool = False):
+        self._check_experts(int(e_end) - int(e_begin))
+        super().set_expert_range(e_begin, e_end, partial, add_shared)
 
     def alloc_rows(self, T: int, stream=None):
         """Buffers of T 8-bit rows, values [T, d] and scales [T, S(d)], for use on `stream`."""
@@ -704,6 +774,8 @@ class DSMoEQ8(DSMoE):
         from an earlier call with as many tokens has it overwritten like the other outputs.
         residual: what the layer's output is added to in place of x."""
         T = x.shape[0]
+        if self.handle in _handles:
+            self._check_experts(_handles[self.handle].experts)
         o = self.alloc_outputs(T, with_scores, stream) if out is None else out
         if x_q is None:
             x_q = o.get("x_q")
