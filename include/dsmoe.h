@@ -610,9 +610,9 @@ dsmoe_status dsmoe_norm_backward(dsmoe_handle* h, int32_t T, const float* dy, co
  * [offsets[0], offsets[E]) are left as they were. Products of e4m3 values and scales are
  * summed in fp32 by the tensor core, which truncates (error 2e-8 of the result's RMS at K = 256,
  * 4e-7 at 7168); the gated product adds chains of at most 2560 of them in fp32, rounded to
- * nearest, so that its 8-bit rows are those of an fp32 sum. Offsets outside [0, R] are clipped to it and a group that would end
- * before it starts is empty, so that nothing outside the tensors is touched; what
- * decreasing offsets leave in rows that two groups share is undefined.
+ * nearest, so that its 8-bit rows are those of an fp32 sum. Offsets outside [0, R] are
+ * clipped to it, and offsets that decrease count as their running maximum: nothing outside the
+ * tensors is touched, and a row that several groups would hold is the first one's.
  *
  * dsmoe_q8_matmul -- out bf16 [R, N] = a W^T, rounded once; N a multiple of 8.
  * dsmoe_q8_gated_matmul -- q, scales: the 8-bit rows [R, N] of SiLU(a W_gate^T) (a W_up^T),

@@ -215,11 +215,21 @@ __device__ __forceinline__ int clipped_offset(const Q8GemmArgs& a, int e) {
   return min(max(__ldg(a.offsets + e), 0), a.R);
 }
 
-// Rows [b, t) of group e, empty where the offsets decrease.
+// Rows [b, t) of group e. Offsets that decrease count as their running maximum, so that the groups
+// are disjoint and a launch has no more tiles than token_tiles allows for. rows: that maximum, or,
+// where shared memory has no room for it, whether the offsets decrease at all.
 template <int kTok>
 __device__ __forceinline__ void group_rows(const Q8GemmArgs& a, const int32_t* rows, int e, int& b, int& t) {
-  b = Geo<kTok>::kRowsInSmem ? rows[e] : clipped_offset(a, e);
-  t = max(Geo<kTok>::kRowsInSmem ? rows[e + 1] : clipped_offset(a, e + 1), b);
+  if (Geo<kTok>::kRowsInSmem) {
+    b = rows[e];
+    t = rows[e + 1];
+  } else {
+    b = clipped_offset(a, e);
+    t = clipped_offset(a, e + 1);
+    if (*rows)
+      for (int i = 0; i < e; ++i) b = max(b, clipped_offset(a, i));
+    t = max(t, b);
+  }
 }
 
 template <int kTok>
@@ -339,9 +349,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
   const int chains = kLong ? q8_chains(kq_all) : kSplit && kGated ? min(q8_chains(kq1 - kq0), G_::kAccs) : 1;
   const int tile0 = kSplit ? blockIdx.x / splits : blockIdx.x, tile_step = kSplit ? gridDim.x / splits : gridDim.x;
 
-  int32_t* group_begin = reinterpret_cast<int32_t*>(base + G_::kOffRows);
-  if (G_::kRowsInSmem)
-    for (int e = threadIdx.x; e <= a.E; e += kThreads) group_begin[e] = clipped_offset(a, e);
+  int32_t* group_begin = reinterpret_cast<int32_t*>(base + (G_::kRowsInSmem ? G_::kOffRows : G_::kOffMisc + 12));
+  bool decreases = false;
+  for (int e = threadIdx.x; e <= a.E; e += kThreads) {
+    const int at = clipped_offset(a, e);
+    decreases |= e < a.E && clipped_offset(a, e + 1) < at;
+    if (G_::kRowsInSmem) group_begin[e] = at;
+  }
   if (threadIdx.x == kThreads - 1) {
     tma_prefetch_desc(&a.map_a);
     tma_prefetch_desc(&a.map_w0);
@@ -370,8 +384,16 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
-  __syncthreads();
+  if (__syncthreads_or(decreases)) {  // rare: the running maximum, or the mark that there is one to take
+    if (!G_::kRowsInSmem) *group_begin = 1;
+    else if (threadIdx.x == 0)
+      for (int e = 1; e <= a.E; ++e) group_begin[e] = max(group_begin[e], group_begin[e - 1]);
+    __syncthreads();
+  } else if (!G_::kRowsInSmem) {
+    *group_begin = 0;
+  }
   if (warp == 0) {  // tile_start[1..E]: the groups' tiles and their inclusive prefix
+    __syncwarp();
     int carry = 0;
     for (int b0 = 0; b0 < a.E; b0 += 32) {
       const int e = b0 + lane;
