@@ -628,6 +628,21 @@ dsmoe_status dsmoe_q8_gated_matmul(dsmoe_handle* h, int32_t E, int64_t R, int32_
                                    void* scales, void* stream);
 
 /*
+ * How a product of these sizes is cut up on a GPU of num_sms SMs (host only, for profiling and
+ * tests). E_all: the experts that the R rows are spread over, E of which are here (E itself for
+ * the two calls above; dsmoe_forward_q8 has R = T K' of all its experts, also for an expert range).
+ */
+typedef enum { DSMOE_Q8_BF16 = 0, DSMOE_Q8_GATED = 1, DSMOE_Q8_FP32 = 2 } dsmoe_q8_output;
+typedef struct dsmoe_q8_tiles {
+  int32_t tokens; /* of a tile: 32, 112, 160 or 240 */
+  int32_t splits; /* CTAs (a cluster) that share a tile along K */
+  int32_t chains; /* parts of K that a CTA sums apart and adds in fp32 */
+  int32_t grid;   /* CTAs */
+} dsmoe_q8_tiles;
+dsmoe_status dsmoe_q8_tiling(int32_t E, int32_t E_all, int64_t R, int32_t N, int32_t K, int32_t output,
+                             int32_t num_sms, dsmoe_q8_tiles* tiles);
+
+/*
  * The layer forward on 8-bit rows and 8-bit expert weights: dsmoe_forward's routing (the
  * bf16 rows x and W_router decide it, so it is the bf16 layer's), the experts' two products
  * as dsmoe_q8_gated_matmul and dsmoe_q8_matmul, and the combine

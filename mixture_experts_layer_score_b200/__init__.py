@@ -14,4 +14,4 @@ from .binding import (DSMoE, DSMoEQ8, DsmoeCfg, DsmoeQ8Weights, DsmoeError, make
                       dsmoe_workspace_tensor, workspace_view, dsmoe_balance_losses,
                       dsmoe_sequence_balance, dsmoe_bias_update, dsmoe_route_noalloc,
                       dsmoe_q8_scale_cols, dsmoe_q8_quantize, dsmoe_q8_quantize_weights, dsmoe_norm_q8,
-                      dsmoe_norm_backward, dsmoe_q8_matmul, dsmoe_q8_gated_matmul, dsmoe_forward_q8)
+                      dsmoe_norm_backward, dsmoe_q8_matmul, dsmoe_q8_gated_matmul, dsmoe_q8_tiling, dsmoe_forward_q8)

@@ -36,7 +36,7 @@ ABI_FUNCTIONS = (
     "dsmoe_ep_combine", "dsmoe_forward_host_async", "dsmoe_host_join", "dsmoe_host_sync", "dsmoe_set_training",
     "dsmoe_backward_experts", "dsmoe_backward_weights", "dsmoe_gemm_role_cycles",
     "dsmoe_q8_scale_cols", "dsmoe_q8_quantize", "dsmoe_q8_quantize_weights", "dsmoe_norm_q8", "dsmoe_norm_backward",
-    "dsmoe_q8_matmul", "dsmoe_q8_gated_matmul", "dsmoe_forward_q8",
+    "dsmoe_q8_matmul", "dsmoe_q8_gated_matmul", "dsmoe_q8_tiling", "dsmoe_forward_q8",
 )
 ROLE_CTAS, ROLE_SLOTS = 160, 9
 ROLE_KINDS = ("gemm_down", "gemm_gate_up", "shared_down", "shared_gate_up", "weight_grad")
@@ -51,11 +51,16 @@ class DsmoeCfg(ctypes.Structure):
                 ("max_tokens", ctypes.c_int32), ("hash_mult", ctypes.c_uint32), ("hash_mod", ctypes.c_uint32)]
 
 
+DSMOE_Q8_BF16, DSMOE_Q8_GATED, DSMOE_Q8_FP32 = range(3)
 Q8_WEIGHTS = ("W_gate", "W_up", "W_down", "Ws_gate", "Ws_up", "Ws_down")
 
 
 class DsmoeQ8Weights(ctypes.Structure):
     _fields_ = [(n + s, ctypes.c_void_p) for n in Q8_WEIGHTS for s in ("", "_scales")]
+
+
+class DsmoeQ8Tiles(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("tokens", "splits", "chains", "grid")]
 
 
 class DsmoeError(RuntimeError):
@@ -123,6 +128,7 @@ def _load():
         "dsmoe_q8_quantize_weights": (ctypes.c_int, [vp, i32, i32, i32] + [vp] * 3 + [vp]),
         "dsmoe_norm_q8": (ctypes.c_int, [vp, i32, vp, vp, vp, ctypes.c_float] + [vp] * 4 + [vp]),
         "dsmoe_norm_backward": (ctypes.c_int, [vp, i32, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp]),
+        "dsmoe_q8_tiling": (ctypes.c_int, [i32, i32, i64, i32, i32, i32, i32, ctypes.POINTER(DsmoeQ8Tiles)]),
         "dsmoe_q8_matmul": (ctypes.c_int, [vp, i32, i64, i32, i32] + [vp] * 6 + [vp]),
         "dsmoe_q8_gated_matmul": (ctypes.c_int, [vp, i32, i64, i32, i32] + [vp] * 9 + [vp]),
     }
@@ -555,6 +561,14 @@ def dsmoe_q8_gated_matmul(handle, E, R, N, K, offsets, a, a_scales, W_gate, gate
         ("W_up", W_up, "q8", nw), ("up_scales", up_scales, "q8", ns), ("q", q, "q8", R * N),
         ("scales", scales, "q8", R * _scale_cols(N)))
     _check(_lib.dsmoe_q8_gated_matmul(handle, E, R, N, K, *p, s), where)
+
+
+def dsmoe_q8_tiling(E, R, N, K, output: int, E_all=None, num_sms: int = 148) -> Dict[str, int]:
+    """How a product is cut up: tokens of a tile, CTAs per tile (splits), chains of K, CTAs (grid)."""
+    t = DsmoeQ8Tiles()
+    _check(_lib.dsmoe_q8_tiling(int(E), int(E if E_all is None else E_all), int(R), int(N), int(K), int(output),
+                                int(num_sms), ctypes.byref(t)), "dsmoe_q8_tiling")
+    return {n: getattr(t, n) for n, _ in t._fields_}
 
 
 def _q8_weight_shapes(cfg: DsmoeCfg):

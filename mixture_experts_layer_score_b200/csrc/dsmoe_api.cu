@@ -1916,13 +1916,15 @@ struct Q8Out {
   float* f32 = nullptr;              // [R, N] = add_bf16 + the product, or itself + the product
   const void* add_bf16 = nullptr;
 };
-dsmoe_status q8_product(dsmoe_handle* h, int32_t E, int64_t R, int32_t N, int32_t K, const int32_t* offsets,
-                        const Q8Rows& a, const Q8Rows& W, const Q8Rows* W1, const Q8Out& out, cudaStream_t s) {
+// E_all: the experts that the R rows are spread over (dsmoe::q8_tiling).
+dsmoe_status q8_product(dsmoe_handle* h, int32_t E, int32_t E_all, int64_t R, int32_t N, int32_t K,
+                        const int32_t* offsets, const Q8Rows& a, const Q8Rows& W, const Q8Rows* W1, const Q8Out& out,
+                        cudaStream_t s) {
   dsmoe::Q8GemmArgs g;
   memset(&g, 0, sizeof(g));
-  int tok = dsmoe::q8_token_tile(R, E, N, K, W1 != nullptr, h->num_sms);
-  if (out.f32) tok = std::min(tok, 112);
-  if (!map_bytes(&g.map_a, a.values, K, R, 1, dsmoe::q8_box_rows(tok)) ||
+  const dsmoe::Q8Tiling t = dsmoe::q8_tiling(
+      R, E, E_all, N, K, W1 ? dsmoe::kQ8Gated : out.f32 ? dsmoe::kQ8F32 : dsmoe::kQ8Bf16, h->num_sms);
+  if (!map_bytes(&g.map_a, a.values, K, R, 1, dsmoe::q8_box_rows(t.tok)) ||
       !(W1 ? map_bytes(&g.map_w0, W.values, K, N, E, 128, true) && map_bytes(&g.map_w1, W1->values, K, N, E, 128, true)
            : map_bytes_pairs(&g.map_w0, W.values, K, N, E)))
     return fail(DSMOE_ERR_CUDA, "cuTensorMapEncodeTiled rejected a tensor map of this call");
@@ -1941,13 +1943,27 @@ dsmoe_status q8_product(dsmoe_handle* h, int32_t E, int64_t R, int32_t N, int32_
   g.add_bf16 = static_cast<const bf16*>(out.add_bf16);
   g.status = h->status;
   g.wait_limit_ns = h->wait_ns;
-  CUDA_TRY(dsmoe::launch_gemm_q8(g, tok, h->num_sms, s));
+  CUDA_TRY(dsmoe::launch_gemm_q8(g, t, s));
   h->launches += 1;
   return DSMOE_OK;
 }
 }  // namespace
 
 DSMOE_EXPORT int32_t dsmoe_q8_scale_cols(int32_t C) { return C > 0 ? dsmoe::q8_scale_cols(C) : 0; }
+
+DSMOE_EXPORT dsmoe_status dsmoe_q8_tiling(int32_t E, int32_t E_all, int64_t R, int32_t N, int32_t K, int32_t output,
+                                          int32_t num_sms, dsmoe_q8_tiles* tiles) {
+  if (!tiles) return fail(DSMOE_ERR_INVALID_ARG, "tiles is NULL");
+  if (output < DSMOE_Q8_BF16 || output > DSMOE_Q8_FP32)
+    return fail(DSMOE_ERR_INVALID_ARG, "output %d is not a dsmoe_q8_output", output);
+  STAGE_TRY(check_q8_dims(R, E, N, K, output == DSMOE_Q8_GATED ? 16 : 8));
+  if (R == 0 || E_all < E || num_sms < 1)
+    return fail(DSMOE_ERR_INVALID_ARG, "%lld rows, %d of %d experts, %d SMs", static_cast<long long>(R), E, E_all,
+                num_sms);
+  const dsmoe::Q8Tiling t = dsmoe::q8_tiling(R, E, E_all, N, K, output, num_sms);
+  *tiles = dsmoe_q8_tiles{t.tok, t.splits, t.chains, t.grid};
+  return DSMOE_OK;
+}
 
 DSMOE_EXPORT dsmoe_status dsmoe_q8_quantize(dsmoe_handle* h, int64_t R, int32_t C, const void* x, void* q,
                                             void* scales, void* stream) {
@@ -2057,7 +2073,7 @@ DSMOE_EXPORT dsmoe_status dsmoe_q8_matmul(dsmoe_handle* h, int32_t E, int64_t R,
   if (!g.ok) return fail(DSMOE_ERR_CUDA, "cannot select device %d", h->device);
   Q8Out o;
   o.bf16 = out;
-  return q8_product(h, E, R, N, K, offsets, {a, a_scales}, {W, W_scales}, nullptr, o,
+  return q8_product(h, E, E, R, N, K, offsets, {a, a_scales}, {W, W_scales}, nullptr, o,
                     static_cast<cudaStream_t>(stream));
 }
 
@@ -2077,7 +2093,7 @@ DSMOE_EXPORT dsmoe_status dsmoe_q8_gated_matmul(dsmoe_handle* h, int32_t E, int6
   Q8Out o;
   o.q = q;
   o.scales = scales;
-  return q8_product(h, E, R, N, K, offsets, {a, a_scales}, {W_gate, gate_scales}, &up, o,
+  return q8_product(h, E, E, R, N, K, offsets, {a, a_scales}, {W_gate, gate_scales}, &up, o,
                     static_cast<cudaStream_t>(stream));
 }
 
@@ -2148,13 +2164,13 @@ dsmoe_status run_forward_q8(dsmoe_handle* h, const FwdQ8Args& q, cudaStream_t s)
       Q8Out o;
       o.q = const_cast<void*>(m.values);
       o.scales = const_cast<void*>(m.scales);
-      STAGE_TRY(q8_product(h, 1, T, Fs, d, nullptr, x, shared_weight(w.Ws_gate, w.Ws_gate_scales, i, Fs, d), &up, o,
-                           h->side));
+      STAGE_TRY(q8_product(h, 1, 1, T, Fs, d, nullptr, x, shared_weight(w.Ws_gate, w.Ws_gate_scales, i, Fs, d), &up,
+                           o, h->side));
       Q8Out o2;
       o2.f32 = h->Hs;
       o2.add_bf16 = i == 0 ? base : nullptr;
-      STAGE_TRY(q8_product(h, 1, T, d, Fs, nullptr, m, shared_weight(w.Ws_down, w.Ws_down_scales, i, d, Fs), nullptr,
-                           o2, h->side));
+      STAGE_TRY(q8_product(h, 1, 1, T, d, Fs, nullptr, m, shared_weight(w.Ws_down, w.Ws_down_scales, i, d, Fs),
+                           nullptr, o2, h->side));
     }
     CUDA_TRY(mark_on(kChainStages + 2, h->side));
     CUDA_TRY(cudaEventRecord(h->ev_join, h->side));
@@ -2174,11 +2190,11 @@ dsmoe_status run_forward_q8(dsmoe_handle* h, const FwdQ8Args& q, cudaStream_t s)
   Q8Out o;
   o.q = a1;
   o.scales = a1_s;
-  STAGE_TRY(q8_product(h, NL, R, F, d, h->offsets + e0, {xp, xp_s}, {w.W_gate, w.W_gate_scales}, &up, o, s));
+  STAGE_TRY(q8_product(h, NL, N, R, F, d, h->offsets + e0, {xp, xp_s}, {w.W_gate, w.W_gate_scales}, &up, o, s));
   CUDA_TRY(mark(5));
   Q8Out o2;
   o2.bf16 = h->Y;
-  STAGE_TRY(q8_product(h, NL, R, d, F, h->offsets + e0, {a1, a1_s}, {w.W_down, w.W_down_scales}, nullptr, o2, s));
+  STAGE_TRY(q8_product(h, NL, N, R, d, F, h->offsets + e0, {a1, a1_s}, {w.W_down, w.W_down_scales}, nullptr, o2, s));
   CUDA_TRY(mark(6));
   if (Ks > 0) CUDA_TRY(cudaStreamWaitEvent(s, h->ev_join, 0));
   FwdArgs fc = a;

@@ -67,8 +67,6 @@ constexpr uint32_t kSfCol0 = kTmemCols - 2 * kSfCols;
 constexpr int kChunk = 8;               // tokens per epilogue chunk
 constexpr uint32_t kStgBytes = 2 * kChunk * kFeat * 4;
 
-enum { kOutBf16 = 0, kOutGated = 1, kOutF32 = 2 };
-
 template <int kTok>
 struct Geo {
   static constexpr uint32_t kAccCols = 2 * kTok;
@@ -311,11 +309,11 @@ __device__ __forceinline__ void add_f32(const Q8GemmArgs& a, int64_t at, float4 
 template <int kOut, int kTok, bool kSplit, bool kLong>
 __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_constant__ Q8GemmArgs a) {
   using G_ = Geo<kTok>;
-  constexpr bool kGated = kOut == kOutGated;
+  constexpr bool kGated = kOut == kQ8Gated;
   constexpr int kTileFeat = kGated ? kFeat : 2 * kFeat;  // output features of a tile
   constexpr int kHold = (kTok / kChunk + 1) / 2;         // chunks of an epilogue group
   constexpr int kRegChunks = kTok > 112 ? 6 : kHold;     // of them (kLong) with their sums in registers
-  static_assert(kOut != kOutF32 || G_::kBufs == 2, "the fp32 output leaves the accumulators late");
+  static_assert(kOut != kQ8F32 || G_::kBufs == 2, "the fp32 output leaves the accumulators late");
   static_assert(!kLong || (kGated && !kSplit), "chains are joined by the epilogue of one CTA");
   static_assert(!kLong || G_::kBufs * G_::kAccCols + 4 * kChunk * (kHold - kRegChunks) <= kSfCol0, "sums of chains");
   static_assert(!kSplit || (kTok % 8 == 0 && kTok * 2 * kFeat * 4 <= G_::kOffSf), "the ring holds the partial sums");
@@ -644,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
       const int n0 = t.n_blk * kTileFeat;
       if constexpr (kSplit) {
         break;  // a cluster has one tile, joined below
-      } else if constexpr (kOut == kOutF32) {
+      } else if constexpr (kOut == kQ8F32) {
         // A thread's two accumulators are neighbours in the output row: a warp's words of a token
         // make one line, stored as they come. What is added is on its way before the
         // accumulators are read.
@@ -890,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_q8_kernel(const __grid_const
         store_gated_rows<1>(a, row, 1, t.n_blk, lane, m);
       } else if (n0 + 8 * lane < a.N) {
         const int64_t at = row * a.N + n0 + 8 * lane;
-        if (kOut == kOutBf16) {
+        if (kOut == kQ8Bf16) {
           *reinterpret_cast<uint4*>(a.out + at) = make_uint4(pack_bf16x2(g.x, u.x), pack_bf16x2(g.y, u.y),
                                                              pack_bf16x2(g.z, u.z), pack_bf16x2(g.w, u.w));
         } else {
@@ -927,25 +925,25 @@ cudaError_t launch_one(const Q8GemmArgs& a, int grid, cudaStream_t s) {
 }
 
 template <int kOut>
-cudaError_t launch_tok(const Q8GemmArgs& a, int tok, int grid, cudaStream_t s) {
-  if (a.splits > 1)
+cudaError_t launch_tok(const Q8GemmArgs& a, const Q8Tiling& t, cudaStream_t s) {
+  const int tok = t.tok, grid = t.grid;
+  if (t.splits > 1)
     return tok == 32 ? launch_one<kOut, 32, true, false>(a, grid, s) : launch_one<kOut, 112, true, false>(a, grid, s);
-  if constexpr (kOut == kOutGated)
-    if (q8_chains((a.K + 511) / 512) > 1)
+  if constexpr (kOut == kQ8Gated)
+    if (t.chains > 1)
       return tok == 32    ? launch_one<kOut, 32, false, true>(a, grid, s)
              : tok == 112 ? launch_one<kOut, 112, false, true>(a, grid, s)
                           : launch_one<kOut, 160, false, true>(a, grid, s);
   if (tok == 32) return launch_one<kOut, 32, false, false>(a, grid, s);
-  if constexpr (kOut != kOutF32)
+  if constexpr (kOut != kQ8F32)
     if (tok == 240) return launch_one<kOut, 240, false, false>(a, grid, s);
   return launch_one<kOut, 112, false, false>(a, grid, s);
 }
 
 // Tiles of `tok` rows that R rows in E groups make at most.
 int64_t token_tiles(int64_t R, int E, int tok) { return (R + (tok - 1) * std::min<int64_t>(E, R)) / tok; }
-}  // namespace
 
-// Token tile by rows per group g = R / E, measured over K = 256 .. 7168 on 32 groups (us, N = 2048
+// Token tile by rows per group g, measured over K = 256 .. 7168 on 32 groups (us, N = 2048
 // unless said):
 //   32   g <= 16 (plain, K = 7168, g = 8: 76.7 against 78.2 with 112; g = 24: 96 against 80), and
 //        where even its tiles are no more than one per SM, each then the shorter (64 groups of
@@ -966,11 +964,12 @@ int64_t token_tiles(int64_t R, int E, int tok) { return (R + (tok - 1) * std::mi
 //        blocks or more (128 rows, gated, K = 7168: 18.7 against 22.3; 256 rows: 26.9 against 30.5;
 //        4 groups of 169 rows, N = 600, K = 3968: 16.6 against 18.7; 13 blocks, 5 groups of 184 rows,
 //        K = 3280, gated: 21.7 against 18.6 the other way).
-static int q8_splits(int64_t tiles, int tok, int K, bool gated, int num_sms);
-int q8_token_tile(int64_t R, int E, int N, int K, bool gated, int num_sms) {
-  const int64_t n_tiles = gated ? (N + 127) / 128 : (N + 255) / 256, g = R / E;
+// Of an expert range (E of E_all groups) g and the tiles are those of the range's share of the rows.
+int q8_splits(int64_t tiles, int tok, int K, bool gated, int num_sms);
+int q8_token_tile(int64_t R, int E, int E_all, int N, int K, bool gated, int num_sms) {
+  const int64_t n_tiles = gated ? (N + 127) / 128 : (N + 255) / 256, g = R / E_all;
   if (g <= 16) return 32;
-  if (std::max<int64_t>(E, (R + 31) / 32) * n_tiles <= num_sms) {
+  if (std::max<int64_t>(E, (R * E / E_all + 31) / 32) * n_tiles <= num_sms) {
     const int kb = (K + kBK - 1) / kBK;
     const int s32 = q8_splits(token_tiles(R, E, 32) * n_tiles, 32, K, gated, num_sms);
     const int s112 = q8_splits(token_tiles(R, E, 112) * n_tiles, 112, K, gated, num_sms);
@@ -987,7 +986,7 @@ int q8_token_tile(int64_t R, int E, int N, int K, bool gated, int num_sms) {
 // 28.9, 18.7, 14.6 and 18.8 (the 16th cluster of 8 runs afterwards). Joining the sums of a
 // 112-token tile takes longer, so there the K loop has to get 14 blocks shorter; two chains of a gated
 // sum are what tensor memory holds of it (of 32 tokens seven, which any K can do with).
-static int q8_splits(int64_t tiles, int tok, int K, bool gated, int num_sms) {
+int q8_splits(int64_t tiles, int tok, int K, bool gated, int num_sms) {
   const int groups = (K + 511) / 512, kb = (K + kBK - 1) / kBK;
   if (tok > 112) return 1;
   for (int s = 8; s > 1; s >>= 1) {
@@ -998,15 +997,27 @@ static int q8_splits(int64_t tiles, int tok, int K, bool gated, int num_sms) {
   return 1;
 }
 
-cudaError_t launch_gemm_q8(const Q8GemmArgs& args, int tok, int num_sms, cudaStream_t s) {
+}  // namespace
+
+Q8Tiling q8_tiling(int64_t R, int E, int E_all, int N, int K, int out, int num_sms) {
+  const bool gated = out == kQ8Gated;
+  const int64_t n_tiles = (N + (gated ? 127 : 255)) / (gated ? 128 : 256);
+  Q8Tiling t;
+  t.tok = q8_token_tile(R, E, E_all, N, K, gated, num_sms);
+  if (out == kQ8F32) t.tok = std::min(t.tok, 112);  // its accumulators are read late: two of them
+  const int64_t bound = token_tiles(R, E, t.tok) * n_tiles;
+  t.splits = q8_splits(bound, t.tok, K, gated, num_sms);
+  t.grid = static_cast<int>(t.splits > 1 ? bound * t.splits : std::min<int64_t>(bound, num_sms));
+  t.chains = gated ? q8_chains(((K + 511) / 512 + t.splits - 1) / t.splits) : 1;
+  if (t.splits > 1) t.chains = std::min(t.chains, t.tok == 32 ? Geo<32>::kAccs : Geo<112>::kAccs);
+  return t;
+}
+
+cudaError_t launch_gemm_q8(const Q8GemmArgs& args, const Q8Tiling& t, cudaStream_t s) {
   Q8GemmArgs a = args;
-  const bool gated = a.q_out != nullptr;
-  const int64_t n_tiles = (a.N + (gated ? 127 : 255)) / (gated ? 128 : 256);
-  const int64_t bound = token_tiles(a.R, a.E, tok) * n_tiles;
-  a.splits = q8_splits(bound, tok, a.K, gated, num_sms);
-  const int grid = static_cast<int>(a.splits > 1 ? bound * a.splits : std::min<int64_t>(bound, num_sms));
-  if (gated) return launch_tok<kOutGated>(a, tok, grid, s);
-  return a.out_f32 ? launch_tok<kOutF32>(a, tok, grid, s) : launch_tok<kOutBf16>(a, tok, grid, s);
+  a.splits = t.splits;
+  if (a.q_out) return launch_tok<kQ8Gated>(a, t, s);
+  return a.out_f32 ? launch_tok<kQ8F32>(a, t, s) : launch_tok<kQ8Bf16>(a, t, s);
 }
 
 }  // namespace dsmoe

@@ -361,15 +361,23 @@ struct Q8GemmArgs {
   uint8_t* q_scales;         // [R, q8_scale_cols(N)]
   float* out_f32;            // [R, N]
   const bf16* add_bf16;      // [R, N] or nullptr
-  int splits;                // set by launch_gemm_q8: CTAs that share a tile along K
+  int splits;                // CTAs that share a tile along K
   uint32_t* status;
   uint64_t wait_limit_ns;
 };
-// Tokens per tile for R rows over E groups, and the row box of map_a: a tile copies the
-// boxes that hold its rows. (The fp32 output takes tiles of at most 112.)
-int q8_token_tile(int64_t R, int E, int N, int K, bool gated, int num_sms);
+// How a product of R rows in E groups is cut up. E_all: the groups that rows of the call's kind are
+// spread over, E where all of them are here (of an expert range, all experts). out: kQ8Bf16, ...
+enum { kQ8Bf16 = 0, kQ8Gated = 1, kQ8F32 = 2 };
+struct Q8Tiling {
+  int tok;     // tokens per tile
+  int splits;  // CTAs (of a cluster) that share a tile along K
+  int chains;  // accumulators that a CTA sums its part of K in, one after another
+  int grid;
+};
+Q8Tiling q8_tiling(int64_t R, int E, int E_all, int N, int K, int out, int num_sms);
+// The row box of map_a: a tile copies the boxes that hold its rows.
 constexpr int q8_box_rows(int tok) { return tok == 240 ? 48 : tok == 160 ? 32 : tok == 112 ? 56 : 16; }
-cudaError_t launch_gemm_q8(const Q8GemmArgs& a, int tok, int num_sms, cudaStream_t s);
+cudaError_t launch_gemm_q8(const Q8GemmArgs& a, const Q8Tiling& t, cudaStream_t s);
 
 // ---------------------------------------------------------------- errors (dsmoe_api.cu)
 // Record the calling thread's last-error message (read back by dsmoe_last_error).
