@@ -1890,6 +1890,13 @@ dsmoe_status check_scales(std::initializer_list<const void*> ptrs) {
   return DSMOE_OK;
 }
 
+dsmoe_status check_offsets(const int32_t* offsets, int32_t E) {
+  if (!offsets && E != 1) return fail(DSMOE_ERR_INVALID_ARG, "offsets is required for E = %d", E);
+  if (reinterpret_cast<uintptr_t>(offsets) & 3u)
+    return fail(DSMOE_ERR_INVALID_ARG, "offsets pointer %p is not 4-byte aligned", static_cast<const void*>(offsets));
+  return DSMOE_OK;
+}
+
 constexpr int kQ8MaxDim = 32768;       // as d_model and d_ff
 constexpr int64_t kQ8MaxRows = 1 << 30;  // as max_tokens * top_k
 
@@ -2065,7 +2072,7 @@ DSMOE_EXPORT dsmoe_status dsmoe_q8_matmul(dsmoe_handle* h, int32_t E, int64_t R,
                                           const void* W_scales, void* out, void* stream) {
   if (!h) return fail(DSMOE_ERR_INVALID_ARG, "handle is NULL");
   STAGE_TRY(check_q8_dims(R, E, N, K, 8));
-  if (!offsets && E != 1) return fail(DSMOE_ERR_INVALID_ARG, "offsets is required for E = %d", E);
+  STAGE_TRY(check_offsets(offsets, E));
   if (R == 0) return DSMOE_OK;
   STAGE_TRY(check_pointers({a, W, out}));
   STAGE_TRY(check_scales({a_scales, W_scales}));
@@ -2083,7 +2090,7 @@ DSMOE_EXPORT dsmoe_status dsmoe_q8_gated_matmul(dsmoe_handle* h, int32_t E, int6
                                                 const void* up_scales, void* q, void* scales, void* stream) {
   if (!h) return fail(DSMOE_ERR_INVALID_ARG, "handle is NULL");
   STAGE_TRY(check_q8_dims(R, E, N, K, 16));
-  if (!offsets && E != 1) return fail(DSMOE_ERR_INVALID_ARG, "offsets is required for E = %d", E);
+  STAGE_TRY(check_offsets(offsets, E));
   if (R == 0) return DSMOE_OK;
   STAGE_TRY(check_pointers({a, W_gate, W_up, q}));
   STAGE_TRY(check_scales({a_scales, gate_scales, up_scales, scales}));

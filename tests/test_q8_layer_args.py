@@ -170,3 +170,12 @@ def test_forward_tensors_are_checked(handle):
     M.dsmoe_set_expert_range(handle, 0, N, M.DSMOE_RANGE_PARTIAL)
     refused(lambda: call(), "h ")
     call(h=f32(T, d))
+
+
+@pytest.mark.parametrize("E", [1, 2])
+@pytest.mark.parametrize("at", [2, 17])
+def test_offsets_that_are_not_aligned_are_refused(E, at):
+    buf = torch.zeros(1 << 13, dtype=torch.uint8)  # a handle of which only the configuration is looked at
+    for call in (lambda: M.dsmoe_q8_matmul(buf.data_ptr(), E, 1, 8, 16, at, *[16] * 5, 0),
+                 lambda: M.dsmoe_q8_gated_matmul(buf.data_ptr(), E, 1, 16, 16, at, *[16] * 8, 0)):
+        refused(call, "offsets", "aligned")
