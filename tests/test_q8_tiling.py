@@ -3,6 +3,7 @@ only a range of the experts is here."""
 import pytest
 
 import mixture_experts_layer_score_b200 as M
+from tests import q8_cases as C
 
 OUT = (M.DSMOE_Q8_BF16, M.DSMOE_Q8_GATED, M.DSMOE_Q8_FP32)
 
@@ -66,3 +67,25 @@ def test_refusals():
                 dict(num_sms=0), dict(output=1, N=8)):
         with pytest.raises(M.DsmoeError):
             M.dsmoe_q8_tiling(**(ok | bad))
+
+
+# ------------------------------------------------------------- what the GPU cases go through
+def test_the_cases_are_the_variants_that_they_name():
+    for output, want, counts, N, K in C.GROUPED:
+        assert C.variant(output, len(counts), sum(counts), N, K) == want, (output, want, N, K)
+        assert want[1] or C.tiles(counts, want[0], N, output) > 148, (output, want, N, K)
+    for want, T, d, Fs, _ in C.SHARED:
+        assert C.variant(C.FP32, 1, T, d, Fs) == want, (want, T, d, Fs)
+
+
+def test_every_variant_has_a_case():
+    """The variants that any sizes lead to, over a grid of them, each have a case on the GPU."""
+    reached = set()
+    for output in OUT:
+        for E in (1,) if output == M.DSMOE_Q8_FP32 else (1, 2, 4, 8, 16, 32, 64, 256, 512):
+            for R in (1, 5, 16, 17, 32, 64, 128, 256, 512, 640, 1008, 1500, 3000, 8192, 65536):
+                for N in (64, 128, 512, 1024, 1280, 2048, 4096, 7168, 9472, 16384):
+                    for K in (16, 128, 512, 704, 1024, 1536, 2048, 2560, 2576, 4096, 4608, 7168, 14336, 32768):
+                        reached.add((output, C.variant(output, E, R, N, K)))
+    cases = {(c[0], c[1]) for c in C.GROUPED} | {(C.FP32, c[0]) for c in C.SHARED}
+    assert reached == cases
