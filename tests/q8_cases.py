@@ -1,5 +1,11 @@
 """Cases of the 8-bit products, one or more for every way in which dsmoe_q8_tiling cuts them up:
-(tokens of a tile, shared by a cluster, summed in several chains)."""
+(tokens of a tile, shared by a cluster, summed in several chains); and their checks against float64.
+
+Tolerances as in tests/test_q8_gpu.py: an fp32 sum of K terms that the tensor core may truncate,
+K 2^-23 of the sum of magnitudes; bf16 half a step, 2^-8; e4m3 half a step, 2^-4 of the value or 2^-10 of
+its block's scale."""
+import torch
+
 import mixture_experts_layer_score_b200 as M
 
 BF16, GATED, FP32 = M.DSMOE_Q8_BF16, M.DSMOE_Q8_GATED, M.DSMOE_Q8_FP32
@@ -45,3 +51,46 @@ def variant(output, E, R, N, K, num_sms=148):
 
 def tiles(counts, tok, N, output):
     return sum(-(-c // tok) for c in counts) * -(-N // (128 if output == GATED else 256))
+
+
+# ------------------------------------------------------------------------ float64 checks
+F8, E8, F64 = torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.float64
+
+
+def values(q, s):
+    """Rows [R, C] or one expert's weights [N, K] (scales of 128 rows) in float64."""
+    s = s.to(F64)
+    if s.shape[0] != q.shape[0]:
+        s = s.repeat_interleave(128, 0)[:q.shape[0]]
+    C = q.shape[1]
+    return q.to(F64) * s[:, :-(-C // 128)].repeat_interleave(128, 1)[:, :C]
+
+
+def sums(a, w):
+    """a w^T in float64, and the error of an fp32 sum of its terms."""
+    return a @ w.T, (a.shape[1] + 2) * 2.0 ** -23 * (a.abs() @ w.abs().T)
+
+
+def check_plain(a, w, out):
+    """bf16 rows of a w^T."""
+    y, err = sums(a, w)
+    assert bool(((out.to(F64) - y).abs() <= 2.0 ** -8 * y.abs() + err).all())
+
+
+def check_gated(a, w_gate, w_up, q, s):
+    """8-bit rows of SiLU(a w_gate^T) (a w_up^T)."""
+    (g, eg), (u, eu) = sums(a, w_gate), sums(a, w_up)
+    silu = g / (1 + torch.exp(-g))
+    m = silu * u
+    # |SiLU'| <= 1.1; exp, the division and the product in fp32 at a few steps each
+    em = 1.1 * eg * u.abs() + (silu.abs() + 1.1 * eg) * eu + 2.0 ** -18 * m.abs()
+    N = m.shape[1]
+    nb = -(-N // 128)
+    assert bool((s.view(torch.uint8)[:, nb:] == 127).all())
+    step = s[:, :nb].to(F64).repeat_interleave(128, 1)[:, :N]
+    half = torch.maximum(2.0 ** -4 * m.abs(), 2.0 ** -10 * step)
+    assert bool(((q.to(F64) * step - m).abs() <= half * (1 + 2.0 ** -4) + em).all())
+    for b in range(nb):  # the smallest power that holds the block, or within the error of it
+        part = slice(128 * b, 128 * b + 128)
+        top, off, p = m[:, part].abs().amax(1), em[:, part].amax(1), s[:, b].to(F64)
+        assert bool((448 * p >= top - off).all() and (448 * (p / 2) <= top + off).all()), b
