@@ -947,7 +947,7 @@ int64_t token_tiles(int64_t R, int E, int tok) { return (R + (tok - 1) * std::mi
 // unless said):
 //   32   g <= 16 (plain, K = 7168, g = 8: 76.7 against 78.2 with 112; g = 24: 96 against 80), and
 //        where even its tiles are no more than one per SM, each then the shorter (64 groups of
-//        56 rows, N = 128, K = 256, gated: 8.3 against 10.5).
+//        56 rows, N = 128, K = 256, gated, in a graph: 6.1 against 7.8).
 //   240  one accumulator, so that the start of a tile's epilogue is exposed, but an MMA at
 //        N = 240 costs 0.5 cycles a token and at N = 112 0.75: from g = 100 on where the K loop is
 //        long enough to bury that start. Gated, 1024 <= K <= 2560 (K = 1024, g = 512: 87 against 99;
@@ -961,9 +961,9 @@ int64_t token_tiles(int64_t R, int E, int tok) { return (R + (tok - 1) * std::mi
 //        in registers). K = 7168, g = 120: 187 against 223 with 112, g = 256: 315 against 343, g = 100:
 //        176 against 166 the other way.
 //   112  the rest, and in place of 32 where its clusters (q8_splits) shorten a CTA's K loop by 14
-//        blocks or more (128 rows, gated, K = 7168: 18.7 against 22.3; 256 rows: 26.9 against 30.5;
-//        4 groups of 169 rows, N = 600, K = 3968: 16.6 against 18.7; 13 blocks, 5 groups of 184 rows,
-//        K = 3280, gated: 21.7 against 18.6 the other way).
+//        blocks or more (in a graph: 128 rows, gated, K = 7168: 17.2 against 19.9; 256 rows: 25.6
+//        against 30.3; 4 groups of 169 rows, N = 600, K = 3968: 14.1 against 16.5; less than 14, 5 groups
+//        of 184 rows, N = 512, K = 3280, gated: 21.4 against 16.9 the other way).
 // Of an expert range (E of E_all groups) g and the tiles are those of the range's share of the rows.
 int q8_splits(int64_t tiles, int tok, int K, bool gated, int num_sms);
 int q8_token_tile(int64_t R, int E, int E_all, int N, int K, bool gated, int num_sms) {
@@ -982,8 +982,8 @@ int q8_token_tile(int64_t R, int E, int E_all, int N, int K, bool gated, int num
 
 // CTAs that share a tile along K: the most of 8, 4, 2 whose clusters run side by side (of 148 SMs,
 // 15 clusters of 8 CTAs, 33 of 4, 74 of 2) and that leave each CTA a group of four K blocks.
-// One row, N = 128, K = 7168, gated: 28.4 us alone, 18.7, 14.0 and 10.5 with 2, 4 and 8; 16 tiles:
-// 28.9, 18.7, 14.6 and 18.8 (the 16th cluster of 8 runs afterwards). Joining the sums of a
+// One row, N = 128, K = 7168, gated, in a graph: 27.2 us alone, 16.2, 11.6 and 8.6 with 2, 4 and 8; 16
+// tiles: 28.6, 18.5, 14.1 and 20.4 (the 16th cluster of 8 runs afterwards). Joining the sums of a
 // 112-token tile takes longer, so there the K loop has to get 14 blocks shorter; two chains of a gated
 // sum are what tensor memory holds of it (of 32 tokens seven, which any K can do with).
 int q8_splits(int64_t tiles, int tok, int K, bool gated, int num_sms) {

@@ -45,7 +45,7 @@ __device__ __forceinline__ uint32_t half_warp_max(uint32_t v) {
 }
 
 // Sixteen lanes hold one block of 128 values, eight each; every thread has kQuantUnits blocks in
-// flight (8192 x 7168: 57 us with one, 36 with two or four, 41 with eight).
+// flight (8192 x 7168, repeated: 43 us with one, 35 with two or four, 41 with eight).
 constexpr int kQuantUnits = 4;
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const bf16* __restrict__ x, uint32_t units, int C,
                                                             uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
@@ -80,8 +80,8 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const bf16* __restri
 
 // One block of threads per 128 x 128 tile of one expert's matrix; the tile stays in registers
 // between the maximum and the encoding (thread: eight columns of rows i, i + 16, ...). Three blocks
-// an SM: 32 x 2048 x 7168 weights in a long run take 226 us (6.2 TB/s) against 235 with four, 261
-// with two and 296 with five.
+// an SM: 32 x 2048 x 7168 weights, calls repeated, take 244 us (5.8 TB/s) against 259 with four, 269
+// with two and 306 with five.
 __global__ void __launch_bounds__(256, 3) quantize_weights_kernel(const bf16* __restrict__ W, int64_t tiles, int N,
                                                                   int K, uint8_t* __restrict__ q,
                                                                   uint8_t* __restrict__ scales) {
@@ -217,7 +217,7 @@ __device__ __forceinline__ uint4 add_bf16x8(const uint4& a, const uint4& b) {
 // registers between the sum of squares and the scaled row u = bf16((r rstd) w); the 8-bit
 // row is that of u, so that it equals the quantisation of the bf16 row. The block loads
 // its next row before it reduces this one. Bound by HBM: 9 bytes a value, 8192 x 7168 in
-// 85-88 us (6.1 TB/s).
+// 87 us in a burst, 89-90 repeated (5.9 TB/s).
 template <int NV>
 __global__ void __launch_bounds__(NV == 1 ? 256 : 512) norm_q8_kernel(const NormArgs a) {
   __shared__ __align__(16) float red[2][32];
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512) norm_q8_kernel(const Norm
     if (t < a.T) load(t);
     block_sums<1>(ss, red[turn]);
     // rounded to nearest: rsqrtf moves 12% more of u's values across a bf16 border (8192 x 7168:
-    // 490 against 440 of 5.9e7), in the same 88 us
+    // 490 against 440 of 5.9e7), in the same time
     const float rstd = __frsqrt_rn(ss[0] / static_cast<float>(d) + a.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -323,8 +323,8 @@ __device__ __forceinline__ void store_share(float* part, int64_t at, const float
 // thread, rows t, t + grid, ... in order. The rows ahead are copied into a ring of kBwdStages
 // rows in shared memory, so that loads stay in flight through the barrier of the row's sums
 // (of r^2 and of w dy r); each warp reads only what it copied itself. Bound by HBM: 10 bytes a
-// value, 16384 x 1280 in 37 us with the kernel that adds the shares (49 us with the rows
-// loaded into registers between the barriers).
+// value, 16384 x 1280 in 40 us with the kernel that adds the shares (with the rows loaded into
+// registers between the barriers it took a quarter longer).
 constexpr int kBwdStages = 3;
 __global__ void __launch_bounds__(1024) norm_backward_kernel(const NormBwdArgs a) {
   extern __shared__ __align__(16) uint4 ring[];
@@ -482,7 +482,7 @@ cudaError_t launch_quantize_weights(const bf16* W, int E, int N, int K, uint8_t*
                                     cudaStream_t s) {
   const int64_t tiles = static_cast<int64_t>(E) * ((N + kQ8Block - 1) / kQ8Block) * ((K + kQ8Block - 1) / kQ8Block);
   // a block per tile: the blocks' phases drift apart and keep the memory busy (32 x 2048 x 7168
-  // weights: 223 us in a short run, against 242 with as many blocks as are resident at once)
+  // weights, repeated: 244 us, against 250 with as many blocks as are resident at once)
   const int64_t grid = std::min<int64_t>(tiles, 1 << 30);
   quantize_weights_kernel<<<static_cast<int>(grid), 256, 0, s>>>(W, tiles, N, K, q, scales);
   return cudaGetLastError();
@@ -501,7 +501,7 @@ cudaError_t launch_permute_q8(const uint8_t* q, const uint8_t* scales, const int
 cudaError_t launch_norm_q8(const NormArgs& a, int num_sms, cudaStream_t s) {
   const int nv = norm_vectors(a.d), threads = norm_threads(a.d);
   // eight blocks per SM, more than are resident at once, so that their phases drift apart (8192
-  // rows of 7168: 87 us against 96 with the resident two and 100 with a block per row)
+  // rows of 7168: 87 us against 94 with the resident two and 101 with a block per row)
   const int grid = static_cast<int>(std::min<int64_t>(a.T, 8 * num_sms));
   if (nv == 1) norm_q8_kernel<1><<<grid, threads, 0, s>>>(a);
   else if (nv == 2) norm_q8_kernel<2><<<grid, threads, 0, s>>>(a);
@@ -516,8 +516,8 @@ int bwd_threads(int d) { return d <= kBwdRingMax ? (d / 8 + 31) / 32 * 32 : 512;
 int bwd_ring_bytes(int d) { return d <= kBwdRingMax ? kBwdStages * bwd_threads(d) * 64 : 0; }
 }  // namespace
 
-// Blocks of the backward pass: about 512 threads per SM (16384 rows of 1280: 37 us, with 1024
-// threads 43; fewer shares of dw to add too), 1024 where a row has more than 320, and about
+// Blocks of the backward pass: about 512 threads per SM (16384 rows of 1280: 40 us, with 1024
+// threads 47; fewer shares of dw to add too), 1024 where a row has more than 320, and about
 // 200 KB of rings.
 int norm_backward_blocks(int64_t T, int d, int num_sms) {
   int per_sm = (bwd_threads(d) > 320 ? 1024 : 512) / bwd_threads(d);
