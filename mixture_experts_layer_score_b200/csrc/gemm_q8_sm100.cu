@@ -37,9 +37,9 @@
 //
 // What bounds it: with few rows the weights' bytes (48 experts of 7168 x 2048 and 144 rows: 109 us,
 // 6.3 TB/s); with many the power limit (gate/up, 8192 rows, 32 experts, d = 7168, F = 2048:
-// 300 us in a burst, 350-355 repeated, 1.36-1.6 PFLOP/s; 265 and 305 with one chain over K, whose
-// sums are coarser); with a short K
-// loop a tile's start and end (32,768 rows, 64 experts, K = 704, N = 1024: 45 us, floor 21).
+// 300-312 us in a burst, 350-367 repeated, 1.3-1.6 PFLOP/s; 265 and 305 with one chain over K, whose
+// sums are coarser) and each drain of a single accumulator (about 6 us of that for one a tile); with a
+// short K loop a tile's start and end (32,768 rows, 64 experts, K = 704, N = 1024: 45-47 us, floor 21).
 // An MMA of M = 128, K = 32 takes max(64 + 0.14 N, N / 2) cycles, hence the large N.
 // The accumulation over K is the tensor core's: fp32, truncating (relative error 4e-7 at
 // K = 7168, which a bf16 or fp32 output of the plain product carries).
@@ -97,7 +97,7 @@ struct Geo {
 
 // The tensor core truncates as it accumulates, so its error grows with the length of the sum: of
 // SwiGLU's values in 8 bits (8192 rows, N = 2048, K = 7168) one chain of MMAs carries 275-332 across
-// an e4m3 border and an fp32 sum 98-119 (K = 2048: 72-81 and 52-60); chains of at most 2048 values,
+// an e4m3 border and an fp32 sum 98-119 (K = 2048: 64-81 and 46-60); chains of at most 2048 values,
 // added in fp32, carry 90-146. A gated sum over `quads` groups of four K blocks takes so many chains
 // (up to 2560 values one); chain_end is the K block after chain i's last (kq0, kq1: the CTA's groups,
 // kb1: its end). Their lengths differ by at most one group.
