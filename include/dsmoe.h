@@ -579,8 +579,8 @@ dsmoe_status dsmoe_q8_quantize_weights(dsmoe_handle* h, int32_t E, int32_t N, in
 /*
  * The root-mean-square norm in front of the layer, for T <= max_tokens rows of d = d_model:
  *   r = bf16(x + residual), u = bf16(r w / sqrt(mean(r^2) + eps)), and the 8-bit rows of u
- * (the row's sum of squares in fp32, which it must not overflow; the 8-bit rows are exactly
- * dsmoe_q8_quantize of u).
+ * (the row's sum of squares in fp32, which it must not overflow, nor underflow where eps is 0: a row
+ * of zeros then gives NaN, 0 / 0; the 8-bit rows are exactly dsmoe_q8_quantize of u).
  *
  * dsmoe_norm_q8
  *     x         bf16 [T, d]
@@ -609,7 +609,7 @@ dsmoe_status dsmoe_norm_backward(dsmoe_handle* h, int32_t T, const float* dy, co
  * within [0, R]; NULL with E = 1 is a plain product of all rows). Output rows outside
  * [offsets[0], offsets[E]) are left as they were. Products of e4m3 values and scales are
  * summed in fp32 by the tensor core, which truncates (error 2e-8 of the result's RMS at K = 256,
- * 4e-7 at 7168); the gated product adds chains of at most 2560 of them in fp32, rounded to
+ * 4e-7 at 7168); the gated product adds chains of at most 2048 of them in fp32, rounded to
  * nearest, so that its 8-bit rows are those of an fp32 sum. Offsets outside [0, R] are
  * clipped to it, and offsets that decrease count as their running maximum: nothing outside the
  * tensors is touched, and a row that several groups would hold is the first one's.

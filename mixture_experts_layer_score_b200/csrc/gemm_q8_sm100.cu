@@ -7,7 +7,7 @@
 // The scales are powers of two, so the tensor core applies them itself (one e8m0 byte per
 // 32 values of K; a block of 128 uses the same byte for its four MMAs) and the fp32
 // accumulator in tensor memory holds the scaled sum over all of K: no partial sum is ever
-// read back to be rescaled. (A gated product with K > 2560 is summed in chains, see q8_chains.)
+// read back to be rescaled. (A gated product with K > 2048 is summed in chains, see q8_chains.)
 //
 // Orientation as in the bf16 grouped GEMM (gemm_sm100.cu): M = 128 output features per chain,
 // N = the tile's tokens rounded up to 16, two chains sharing the token operand (gated: the
@@ -98,13 +98,11 @@ struct Geo {
 // The tensor core truncates as it accumulates, so its error grows with the length of the sum: of
 // SwiGLU's values in 8 bits (8192 rows, N = 2048, K = 7168) one chain of MMAs carries 275-332 across
 // an e4m3 border and an fp32 sum 98-119 (K = 2048: 64-81 and 46-60); chains of at most 2048 values,
-// added in fp32, carry 90-146. A gated sum over `quads` groups of four K blocks takes so many chains
-// (up to 2560 values one); chain_end is the K block after chain i's last (kq0, kq1: the CTA's groups,
-// kb1: its end). Their lengths differ by at most one group.
+// added in fp32, carry 90-146. A gated sum over `quads` groups of four K blocks takes so many chains;
+// chain_end is the K block after chain i's last (kq0, kq1: the CTA's groups, kb1: its end). Their
+// lengths differ by at most one group.
 constexpr int kChainQuads = 4;
-__host__ __device__ __forceinline__ int q8_chains(int quads) {
-  return quads <= kChainQuads + 1 ? 1 : (quads + kChainQuads - 1) / kChainQuads;
-}
+__host__ __device__ __forceinline__ int q8_chains(int quads) { return (quads + kChainQuads - 1) / kChainQuads; }
 __device__ __forceinline__ int chain_end(int kq0, int kq1, int chains, int i, int kb1) {
   return min(4 * (kq0 + (i + 1) * (kq1 - kq0) / chains), kb1);
 }
@@ -950,13 +948,13 @@ int64_t token_tiles(int64_t R, int E, int tok) { return (R + (tok - 1) * std::mi
 //        56 rows, N = 128, K = 256, gated, in a graph: 6.1 against 7.8).
 //   240  one accumulator, so that the start of a tile's epilogue is exposed, but an MMA at
 //        N = 240 costs 0.5 cycles a token and at N = 112 0.75: from g = 100 on where the K loop is
-//        long enough to bury that start. Gated, 1024 <= K <= 2560 (K = 1024, g = 512: 87 against 99;
+//        long enough to bury that start. Gated, 1024 <= K <= 2048 (K = 1024, g = 512: 87 against 99;
 //        K = 2048, g = 120: 62.8 against 67.5; K = 704, g = 300: 61 against 57 the other way).
 //        Plain, whose 112-token tiles run two accumulators over a cheaper epilogue, K >= 4096
 //        (K = 7168, g = 100: 98.8 against 107), or g >= 240 with g K >= 350,000 (K = 1280,
 //        g = 512: 53.8 against 61.1; K = 2048, g = 200: 45.4 against 43.3 and K = 448, g = 512:
 //        35.2 against 33.4 the other way).
-//   160  gated, K > 2560, from g = 110 on: the sums of two chains and more have to be kept, and those
+//   160  gated, K > 2048, from g = 110 on: the sums of two chains and more have to be kept, and those
 //        of 240 tokens have no place in registers and tensor memory (of 160: 6 of a group's 10 chunks
 //        in registers). K = 7168, g = 120: 187 against 223 with 112, g = 256: 315 against 343, g = 100:
 //        176 against 166 the other way.

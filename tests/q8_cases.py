@@ -28,10 +28,10 @@ GROUPED = [  # output, variant, rows of each expert, N, K; where not clustered m
     (GATED, (112, False, True), SIXTY, 1296, 2832),
     (GATED, (112, True, False), [250, 260, 240, 258], 80, 4608),
     (GATED, (112, True, True), [47, 90, 3, 48] * 8, 64, 7168),
-    (GATED, (160, False, True), LARGE, 2064, 2832),
+    (GATED, (160, False, True), LARGE, 2064, 2064),
     (GATED, (160, False, True), LARGE, 1936, 7168),
     (GATED, (240, False, False), [511, 240, 241, 16], 2832, 1296),
-    (GATED, (240, False, False), LARGE, 2064, 2560),
+    (GATED, (240, False, False), LARGE, 2064, 2048),
 ]
 
 SHARED = [  # variant of the fp32 product, tokens, d, F_s, shared experts

@@ -39,8 +39,10 @@ def encode(m):
     return torch.round(v / step) * step, s
 
 
-# counts of each expert, N, K, repetitions: 112-token tiles, 32-token tiles, clusters of two CTAs
-CASES = [([2048, 2100, 1996, 2048], 2048, 7168, 1), ([16] * 64, 2048, 32768, 1), ([32], 9472, 32768, 8)]
+# counts of each expert, N, K, repetitions: 160-token tiles, 32-token tiles, clusters of two CTAs; the
+# longest sum of one chain (240-token tiles); 112-token tiles
+CASES = [([2048, 2100, 1996, 2048], 2048, 7168, 1), ([16] * 64, 2048, 32768, 1), ([32], 9472, 32768, 8),
+         ([2048, 2100, 1996, 2048], 2048, 2048, 2), ([80, 90, 108, 100] * 8, 2048, 8192, 2)]
 
 
 @pytest.mark.parametrize("counts,N,K,times", CASES)

@@ -49,13 +49,13 @@ def test_every_row_has_a_tile(output):
 @pytest.mark.parametrize("K", [128, 2048, 2560, 2561 + 15, 4096, 7168, 16384, 32768])
 @pytest.mark.parametrize("E,R", [(1, 1), (1, 128), (4, 676), (32, 600), (32, 3300), (32, 8192)])
 def test_chains_of_a_gated_sum_are_short(K, E, R):
-    """At most 2560 values in one accumulator, whatever shares K (a group of 512 more where it does
+    """At most 2048 values in one accumulator, whatever shares K (a group of 512 more where it does
     not divide: 32 tokens in clusters of two and K = 32768)."""
     K = K // 16 * 16
     for N in (128, 512, 2048, 9472):
         t = M.dsmoe_q8_tiling(E, R, N, K, M.DSMOE_Q8_GATED)
         groups = -(-(-(-K // 512)) // t["splits"])
-        assert -(-groups // t["chains"]) <= 5, t
+        assert -(-groups // t["chains"]) <= (5 if (K, t["tokens"], t["splits"]) == (32768, 32, 2) else 4), t
         assert t["tokens"] != 240 or t["chains"] == 1
         assert M.dsmoe_q8_tiling(E, R, N, K, M.DSMOE_Q8_BF16)["chains"] == 1
 
