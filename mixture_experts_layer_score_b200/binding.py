@@ -578,13 +578,13 @@ def _q8_weight_shapes(cfg: DsmoeCfg):
             "Ws_gate": (Ks, Fs, d), "Ws_up": (Ks, Fs, d), "Ws_down": (Ks, d, Fs)}
 
 
-def _take_q8_weights(where: str, handle, weights: Dict, experts: int) -> DsmoeQ8Weights:
+def _take_q8_weights(where: str, handle, weights: Dict, experts: Optional[int]) -> DsmoeQ8Weights:
     """The struct of 8-bit weights given as (values, scales) pairs by name, each checked against
-    the handle's configuration and the number of routed experts."""
+    the handle's configuration and the number of routed experts (raw addresses pass)."""
     ptrs = []
     for name, (E, N, K) in _q8_weight_shapes(_handles[handle].cfg).items():
-        E = experts if E is None else E
-        values, scales = (E and weights.get(name)) or (None, None)
+        values, scales = (E != 0 and weights.get(name)) or (None, None)  # (0: no shared experts)
+        E = (experts or 0) if E is None else E
         for what, t, rows, cols in (("values", values, N, K), ("scales", scales, -(-N // 128), _scale_cols(K))):
             if getattr(t, "ndim", 0) == 3 and tuple(t.shape) != (E, rows, cols):
                 raise DsmoeError(DSMOE_ERR_INVALID_ARG, where,
@@ -764,7 +764,7 @@ class DSMoEQ8(DSMoE):
             self.q[name] = tuple(W)
         if any(n in weights and not isinstance(weights[n], (tuple, list)) for n in Q8_WEIGHTS):
             torch.cuda.current_stream(device).synchronize()  # the weights are ready for forwards on any stream
-        self._weights = _take_q8_weights(where, self.handle, self.q, self.experts or 0)
+        self._weights = _take_q8_weights(where, self.handle, self.q, self.experts)
 
     def _check_experts(self, experts: int):
         if self.experts is not None and self.experts != experts:

@@ -131,6 +131,8 @@ def test_layer_takes_what_fits(handle):
         refused(lambda: M.DSMoEQ8(BIG, bf16 | {k: v}), k)
     flat = {k: tuple(t.reshape(-1) for t in v) for k, v in pairs().items()}
     assert M.DSMoEQ8(BIG, flat).experts == N
+    raw = M.DSMoEQ8(BIG, {k: (16, 32) for k in pairs()})  # addresses are taken as they are
+    assert raw.experts is None and raw._weights.W_up == 16 and raw._weights.Ws_down_scales == 32
     no_shared = M.make_cfg(d_model=d, n_routed=N, top_k=2, d_ff=F, max_tokens=8)
     B._handles[handle].cfg = no_shared
     layer = M.DSMoEQ8(no_shared, pairs())  # (shared experts that the configuration does not have are not read)
